@@ -83,6 +83,11 @@ typedef enum { TRTV_BF16 = 0, TRTV_FP8_E4M3 = 1, TRTV_F32 = 2 } trtv_dtype;
 #define TRTV_DEVERR_BLOCK_IDX 4 /* a top-k block index >= max_pages_per_req */
 #define TRTV_DEVERR_TIMEOUT 8   /* a pipeline wait gave up (2 s, or the limit set by
                                    trtv_test_withhold_pages): that call's results are invalid */
+#define TRTV_DEVERR_INDPTR 16   /* qo_indptr is not ascending from 0, ends past num_tokens, or gives a
+                                   request more than qo_len tokens */
+#define TRTV_DEVERR_POSITION 32 /* a token's rotary position outside [0, table_len) */
+#define TRTV_DEVERR_PATH 64     /* an accepted path that is not strictly ascending, leaves its tree
+                                   or is longer than it */
 
 typedef struct {
   int32_t batch;             /* requests B >= 1 */
@@ -347,6 +352,134 @@ trtv_status trtv_draft_attn_p32(const trtv_geom* geom, const void* q, const void
                                 const int32_t* k_sub, const int32_t* v_sub, const int32_t* kv_lens,
                                 void* out, int32_t out_dtype, void* workspace, size_t ws_bytes,
                                 void* stream);
+
+/*
+ * ---- Packed token rows: staging, prompts, trees, commits ------------------
+ * The calls below take the new tokens of all requests as packed rows, with a
+ * different number of tokens n_b per request:
+ *   qo_indptr  int32 [batch + 1] (read on the device), qo_indptr[0] = 0: the
+ *              rows of request b are qo_indptr[b] .. qo_indptr[b + 1] - 1.
+ *              NULL: every request has n_b = geom->qo_len rows.
+ *   num_tokens rows of the row-indexed buffers, >= qo_indptr[batch] (with
+ *              qo_indptr NULL: >= batch * qo_len).  Output rows behind the
+ *              last request's are left as they were.  0: the call does nothing.
+ *   geom->qo_len  the most tokens of any request (grids and kernels are chosen
+ *              by it): n_b <= qo_len.
+ * kv_len counts the new tokens: token t of request b is cache position
+ * c_b + t with c_b = kv_len[b] - n_b.  A request with n_b = 0 takes no part
+ * (its length is not checked).  head_dim 64 or 128 (FP8 caches: 128),
+ * num_q_heads / num_kv_heads <= 128, batch <= 4096.
+ * A request whose qo_indptr entries are not ascending within
+ * [0, num_tokens], or give more than qo_len tokens, is left out
+ * (TRTV_DEVERR_INDPTR); one with kv_len < n_b or beyond 128 * max_pages_per_req
+ * sets TRTV_DEVERR_KV_LEN.
+ */
+
+/* Inputs of trtv_norm_rope_stage (device pointers; strides in elements). */
+typedef struct {
+  const void* q;             /* bf16 [num_tokens, num_q_heads, head_dim], row pitch q_stride */
+  const void* k;             /* bf16 [num_tokens, num_kv_heads, head_dim], row pitch k_stride */
+  const void* v;             /* as k, row pitch v_stride */
+  int64_t q_stride;          /* elements from one token's row to the next (multiples of 8, at */
+  int64_t k_stride;          /* least heads * head_dim): the three may be views of one */
+  int64_t v_stride;          /* [num_tokens, (Hq + 2 Hk) * head_dim] projection */
+  const void* q_weight;      /* bf16 [head_dim], or NULL: q is not normed */
+  const void* k_weight;      /* bf16 [head_dim], or NULL: k is not normed */
+  const float* rope_table;   /* f32 [table_len, rot_dim]: rot_dim / 2 cosines, then the sines */
+  const int32_t* positions;  /* int32 [num_tokens] row of rope_table per token, or NULL: the
+                                token's cache position */
+  int32_t table_len;
+  int32_t rot_dim;           /* rotated leading dims of a head: a multiple of 8, <= head_dim;
+                                0: no rotation (rope_table is not read) */
+  int32_t interleaved;       /* 0: dim i turns with i + rot_dim / 2; 1: dim 2i with 2i + 1 */
+  float eps;                 /* of the norm, >= 0 */
+} trtv_norm_rope;
+
+/*
+ * Norm and rotation of the new tokens' queries and keys, and KV staging, in
+ * one pass.  For every head of q (k):
+ *   y = x * (mean(x^2) + eps)^(-1/2) * q_weight (k_weight), then for i <
+ *   rot_dim / 2 with (c, s) = (rope_table[pos][i], rope_table[pos][rot_dim / 2 + i])
+ *   (y1, y2) -> (y1 c - y2 s, y2 c + y1 s), (y1, y2) the i-th pair.
+ * All in binary32 with one rounding at the end: q_out gets bf16; the cache row
+ * of the token's position (as trtv_stage_kv) gets the key as bf16, or as
+ * E4M3(y / k_scale), and the value's bits, or E4M3(v / v_scale) (binary32
+ * quotient, round to nearest even, saturated to +-448, NaN kept).
+ *   q_out      bf16 [num_tokens, num_q_heads, head_dim] (written), may be q
+ *              itself when q_stride = num_q_heads * head_dim
+ * All pointers 16-byte aligned, but page_table, kv_lens, qo_indptr and
+ * positions (4).  A token with a position outside the table gets a zero q_out
+ * row and is not staged (TRTV_DEVERR_POSITION); a request with a bad kv_len
+ * likewise; a token whose page names no slot of the pool is not staged
+ * (TRTV_DEVERR_PAGE_ID), its q_out row is written.
+ */
+trtv_status trtv_norm_rope_stage(const trtv_geom* geom, const trtv_norm_rope* in, const int32_t* qo_indptr,
+                                 int32_t num_tokens, void* q_out, void* kv_pool, const int32_t* page_table,
+                                 const int32_t* kv_lens, void* stream);
+
+/*
+ * Workspace bytes of trtv_prompt_attn and trtv_verify_tree for this geometry;
+ * 0 on a geometry that they refuse.  Caller-allocated, 256-byte aligned, no
+ * initial contents required; calls that may overlap must not share one.
+ */
+size_t trtv_workspace_bytes_rows(const trtv_geom* geom);
+
+/*
+ * Causal attention of packed prompts (or chunks of prompts behind a cached
+ * prefix) over the paged cache that holds their keys and values:
+ *   out[row of t][hq] = sum_{p <= c_b + t} softmax_p(x) v_p, x and v as in
+ *   trtv_verify_dense (for equal n_b <= 32 the two agree up to rounding).
+ * The causal bound is the verify ladder's ("... verify" commit: inclusive
+ * causal bound with offset kv_len - qo_len), for any number of tokens.
+ *   q          bf16 [num_tokens, num_q_heads, head_dim], 16-byte aligned
+ *   out        as q, bf16 or f32 (out_dtype), 16-byte aligned (written)
+ *   kv_pool    16-byte aligned; a bad page id reads slot 0 instead
+ *              (TRTV_DEVERR_PAGE_ID; finite but meaningless rows)
+ * A request with a bad kv_len gets zero rows.  Keys and values at or past
+ * kv_len are never used, whatever they hold; a value that is not finite at a
+ * position below kv_len may reach any row of its request.  FP8 caches: as
+ * trtv_verify_dense.
+ */
+trtv_status trtv_prompt_attn(const trtv_geom* geom, const void* q, const void* kv_pool, const int32_t* page_table,
+                             const int32_t* kv_lens, const int32_t* qo_indptr, int32_t num_tokens, void* out,
+                             int32_t out_dtype, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Attention of a tree of drafted tokens over the cache: as trtv_prompt_attn,
+ * but token t of request b attends the c_b positions before the tree and, of
+ * the tree, the positions c_b + j whose bit is set in its mask:
+ *   tree_mask  uint32 [num_tokens, ceil(geom->qo_len / 32)]: bit j % 32 of
+ *              word j / 32 of a token's row lets it attend tree node j (a
+ *              token attends itself only if its own bit is set); bits at
+ *              n_b and above are ignored.
+ * Any mask is allowed (a tree's has every node's ancestors and the node
+ * itself); a row that sees no position is zero.  qo_len <= 128.
+ */
+trtv_status trtv_verify_tree(const trtv_geom* geom, const void* q, const void* kv_pool, const int32_t* page_table,
+                             const int32_t* kv_lens, const int32_t* qo_indptr, int32_t num_tokens,
+                             const uint32_t* tree_mask, void* out, int32_t out_dtype, void* workspace,
+                             size_t ws_bytes, void* stream);
+
+/*
+ * After a tree is verified: the K and V rows of the accepted path move to the
+ * front of the tree's cache positions, in path order, and the length shrinks
+ * to what is kept:
+ *   cache row c_b + i <- cache row c_b + path[b][i] for i < path_len[b],
+ *   new_kv_lens[b] = c_b + path_len[b].
+ *   path       int32 [batch, max_path]: strictly ascending tree nodes (a
+ *              node's parent has a smaller index); entries from path_len on
+ *              are not read
+ *   path_len   int32 [batch], 0 <= path_len[b] <= min(n_b, max_path)
+ *   new_kv_lens int32 [batch] (written), may be kv_lens itself
+ * Rows at or past the new length keep what they held.  A request with a bad
+ * path (TRTV_DEVERR_PATH), kv_len or qo_indptr entry, or whose tree touches a
+ * page that names no slot (TRTV_DEVERR_PAGE_ID), is not moved and keeps its
+ * length, as does one without tokens.  qo_len <= 128.
+ */
+trtv_status trtv_tree_commit(const trtv_geom* geom, void* kv_pool, const int32_t* page_table,
+                             const int32_t* kv_lens, const int32_t* qo_indptr,
+                             const int32_t* path, const int32_t* path_len, int32_t max_path,
+                             int32_t* new_kv_lens, void* stream);
 
 /*
  * Test hook for the bounded waits (the CUDA-graphs commit of "Eagle3 for M3

@@ -22,12 +22,14 @@ __all__ = [
     "trtv_verify_dense_noalloc", "trtv_stage_kv", "trtv_flatten_page_table",
     "trtv_page_table_from_flat", "trtv_workspace_bytes_flat", "trtv_verify_dense_flat",
     "trtv_draft_attn_p32", "trtv_msa_select", "trtv_msa_verify", "trtv_status_string",
-    "trtv_test_withhold_pages", "geom_of", "EXPORTS",
+    "trtv_test_withhold_pages", "trtv_norm_rope_stage", "trtv_workspace_bytes_rows", "trtv_prompt_attn",
+    "trtv_verify_tree", "trtv_tree_commit", "NormRope", "geom_of", "EXPORTS",
 ]
 
 TRTV_OK, TRTV_ERR_INVALID_ARG, TRTV_ERR_UNSUPPORTED, TRTV_ERR_CUDA, TRTV_ERR_WORKSPACE = range(5)
 TRTV_BF16, TRTV_FP8_E4M3, TRTV_F32 = 0, 1, 2
 DEVERR_KV_LEN, DEVERR_PAGE_ID, DEVERR_BLOCK_IDX, DEVERR_TIMEOUT = 1, 2, 4, 8
+DEVERR_INDPTR, DEVERR_POSITION, DEVERR_PATH = 16, 32, 64
 
 # every function the C header declares
 EXPORTS = ("trtv_status_string", "trtv_version", "trtv_subpage_view", "trtv_workspace_bytes",
@@ -35,7 +37,8 @@ EXPORTS = ("trtv_status_string", "trtv_version", "trtv_subpage_view", "trtv_work
            "trtv_msa_sparse_attn", "trtv_stage_kv", "trtv_flatten_page_table",
            "trtv_page_table_from_flat", "trtv_workspace_bytes_flat", "trtv_verify_dense_flat",
            "trtv_draft_attn_p32", "trtv_msa_select", "trtv_msa_verify", "trtv_test_withhold_pages",
-           "trtv_get_device_error")
+           "trtv_get_device_error", "trtv_norm_rope_stage", "trtv_workspace_bytes_rows", "trtv_prompt_attn",
+           "trtv_verify_tree", "trtv_tree_commit")
 
 
 class TrtvError(RuntimeError):
@@ -53,6 +56,15 @@ class Geom(ctypes.Structure):
                 ("kv_dtype", ctypes.c_int32), ("sm_scale", ctypes.c_float),
                 ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float),
                 ("num_ctas", ctypes.c_int32)]
+
+
+class NormRope(ctypes.Structure):
+    """Mirror of ``trtv_norm_rope``."""
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("rope_table", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("table_len", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -114,6 +126,16 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     h.trtv_get_device_error.argtypes = [ctypes.POINTER(ctypes.c_int32), vp]
     h.trtv_test_withhold_pages.restype = ctypes.c_int
     h.trtv_test_withhold_pages.argtypes = [i32, ctypes.c_uint32]
+    h.trtv_norm_rope_stage.restype = ctypes.c_int
+    h.trtv_norm_rope_stage.argtypes = [G, ctypes.POINTER(NormRope), vp, i32, vp, vp, vp, vp, vp]
+    h.trtv_workspace_bytes_rows.restype = sz
+    h.trtv_workspace_bytes_rows.argtypes = [G]
+    h.trtv_prompt_attn.restype = ctypes.c_int
+    h.trtv_prompt_attn.argtypes = [G, vp, vp, vp, vp, vp, i32, vp, i32, vp, sz, vp]
+    h.trtv_verify_tree.restype = ctypes.c_int
+    h.trtv_verify_tree.argtypes = [G, vp, vp, vp, vp, vp, i32, vp, vp, i32, vp, sz, vp]
+    h.trtv_tree_commit.restype = ctypes.c_int
+    h.trtv_tree_commit.argtypes = [G, vp, vp, vp, vp, vp, vp, i32, vp, vp]
     _lib = h
     return h
 
@@ -275,3 +297,146 @@ def trtv_get_device_error(stream=None) -> int:
     v = ctypes.c_int32(0)
     _check("trtv_get_device_error", load().trtv_get_device_error(ctypes.byref(v), _stream(stream)))
     return v.value
+
+
+# -- packed token rows -------------------------------------------------------
+# These calls know their tensors' shapes, so they check them: a buffer that is
+# too small for the geometry would be read out of bounds on the device.
+
+def _arg(fn: str, name: str, x, dtype, shape, none_ok: bool = False, at_least: bool = False) -> int:
+    """Pointer of a contiguous CUDA tensor of `dtype` (one of several) and `shape` (a None entry: any;
+    at_least: or more entries along the first axis)."""
+    if x is None and none_ok:
+        return 0
+    if isinstance(x, int):
+        return x
+    p = _ptr(x)
+    if p and x.get_device() != _device():
+        raise ValueError(f"{fn}: {name} is on cuda:{x.get_device()}, the current device is cuda:{_device()}")
+    if x.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError(f"{fn}: {name} is {x.dtype}, expected {dtype}")
+    s = tuple(x.shape)
+    if len(s) != len(shape) or any(
+            w is not None and (g < w if at_least and i == 0 else g != w) for i, (g, w) in enumerate(zip(s, shape))):
+        raise ValueError(f"{fn}: {name} has shape {s}, expected {shape}{' or more rows' if at_least else ''}")
+    return p
+
+
+def _device() -> int:
+    import torch
+    return torch.cuda.current_device()
+
+
+def _rows_arg(fn: str, name: str, x, rows, heads: int, dim: int):
+    """Pointer and row pitch of a bf16 [rows, heads, dim] tensor whose rows may lie apart."""
+    import torch
+    if x is None or not x.is_cuda:
+        raise ValueError(f"{fn}: {name} is not a CUDA tensor")
+    if x.get_device() != _device():
+        raise ValueError(f"{fn}: {name} is on cuda:{x.get_device()}, the current device is cuda:{_device()}")
+    if x.dtype != torch.bfloat16 or x.dim() != 3 or tuple(x.shape) != (rows, heads, dim):
+        raise ValueError(f"{fn}: {name} is {x.dtype} {tuple(x.shape)}, expected bf16 {(rows, heads, dim)}")
+    if x.stride(2) != 1 or (heads > 1 and x.stride(1) != dim):
+        raise ValueError(f"{fn}: {name}'s heads of one token are not contiguous")
+    return x.data_ptr(), x.stride(0) if rows > 1 else heads * dim
+
+
+def _pool_arg(fn: str, geom: Geom, x) -> int:
+    import torch
+    if isinstance(x, int):
+        return x
+    fp8 = geom.kv_dtype == TRTV_FP8_E4M3
+    p = _ptr(x)
+    if x.get_device() != _device():
+        raise ValueError(f"{fn}: kv_pool is on cuda:{x.get_device()}, the current device is cuda:{_device()}")
+    if x.dtype not in ((torch.uint8, torch.float8_e4m3fn) if fp8 else (torch.bfloat16,)):
+        raise ValueError(f"{fn}: kv_pool is {x.dtype}")
+    need = geom.num_slots * geom.slot_stride * 128 * geom.num_kv_heads * geom.head_dim
+    if x.numel() < need:
+        raise ValueError(f"{fn}: kv_pool holds {x.numel()} elements, the geometry needs {need}")
+    return p
+
+
+def _tables(fn: str, geom: Geom, page_table, kv_lens, qo_indptr):
+    import torch
+    return (_arg(fn, "page_table", page_table, torch.int32, (geom.batch, geom.max_pages_per_req)),
+            _arg(fn, "kv_lens", kv_lens, torch.int32, (geom.batch,)),
+            _arg(fn, "qo_indptr", qo_indptr, torch.int32, (geom.batch + 1,), none_ok=True))
+
+
+def trtv_norm_rope_stage(geom: Geom, q, k, v, q_weight, k_weight, eps: float, rope_table, rot_dim: int,
+                         interleaved: bool, positions, qo_indptr, q_out, kv_pool, page_table, kv_lens,
+                         stream=None) -> None:
+    """Per-head norm of queries and keys, rotation, and K/V staging of packed token rows: q [rows, Hq, D],
+    k, v [rows, Hk, D] bf16, each possibly a view of one projection; q_out [rows, Hq, D] bf16."""
+    import torch
+    fn = "trtv_norm_rope_stage"
+    rows, D = q.shape[0], geom.head_dim
+    a = NormRope(eps=eps, rot_dim=rot_dim, interleaved=int(interleaved),
+                 table_len=0 if rope_table is None else rope_table.shape[0])
+    a.q, a.q_stride = _rows_arg(fn, "q", q, rows, geom.num_q_heads, D)
+    a.k, a.k_stride = _rows_arg(fn, "k", k, rows, geom.num_kv_heads, D)
+    a.v, a.v_stride = _rows_arg(fn, "v", v, rows, geom.num_kv_heads, D)
+    a.q_weight = _arg(fn, "q_weight", q_weight, torch.bfloat16, (D,), none_ok=True)
+    a.k_weight = _arg(fn, "k_weight", k_weight, torch.bfloat16, (D,), none_ok=True)
+    a.rope_table = _arg(fn, "rope_table", rope_table, torch.float32, (None, rot_dim), none_ok=True)
+    a.positions = _arg(fn, "positions", positions, torch.int32, (rows,), none_ok=True)
+    pt, kl, ip = _tables(fn, geom, page_table, kv_lens, qo_indptr)
+    _check(fn, load().trtv_norm_rope_stage(
+        ctypes.byref(geom), ctypes.byref(a), ip, rows,
+        _arg(fn, "q_out", q_out, torch.bfloat16, (rows, geom.num_q_heads, D)), _pool_arg(fn, geom, kv_pool), pt, kl,
+        _stream(stream)))
+
+
+def trtv_workspace_bytes_rows(geom: Geom) -> int:
+    return load().trtv_workspace_bytes_rows(ctypes.byref(geom))
+
+
+def _ws_arg(fn: str, workspace, ws_bytes: int) -> int:
+    if isinstance(workspace, int):
+        return workspace
+    if workspace.get_device() != _device() or workspace.numel() * workspace.element_size() < ws_bytes:
+        raise ValueError(f"{fn}: workspace on {workspace.device} of {workspace.numel() * workspace.element_size()} bytes, "
+                         f"expected {ws_bytes} on cuda:{_device()}")
+    return _ptr(workspace)
+
+
+def _rows_attn_args(fn: str, geom: Geom, q, kv_pool, page_table, kv_lens, qo_indptr, out, out_dtype: int):
+    import torch
+    rows = q.shape[0]
+    shape = (rows, geom.num_q_heads, geom.head_dim)
+    pt, kl, ip = _tables(fn, geom, page_table, kv_lens, qo_indptr)
+    return (ctypes.byref(geom), _arg(fn, "q", q, torch.bfloat16, shape), _pool_arg(fn, geom, kv_pool), pt, kl, ip, rows,
+            _arg(fn, "out", out, torch.float32 if out_dtype == TRTV_F32 else torch.bfloat16, shape))
+
+
+def trtv_prompt_attn(geom: Geom, q, kv_pool, page_table, kv_lens, qo_indptr, out, out_dtype: int, workspace,
+                     ws_bytes: int, stream=None) -> None:
+    """Causal attention of packed prompts (q, out [rows, Hq, D]) over the paged cache."""
+    *a, o = _rows_attn_args("trtv_prompt_attn", geom, q, kv_pool, page_table, kv_lens, qo_indptr, out, out_dtype)
+    _check("trtv_prompt_attn", load().trtv_prompt_attn(*a, o, out_dtype, _ws_arg("trtv_prompt_attn", workspace, ws_bytes), ws_bytes,
+                                                           _stream(stream)))
+
+
+def trtv_verify_tree(geom: Geom, q, kv_pool, page_table, kv_lens, qo_indptr, tree_mask, out, out_dtype: int,
+                     workspace, ws_bytes: int, stream=None) -> None:
+    """Attention of drafted trees over the paged cache; tree_mask int32 [rows, ceil(qo_len / 32)]."""
+    import torch
+    fn = "trtv_verify_tree"
+    *a, o = _rows_attn_args(fn, geom, q, kv_pool, page_table, kv_lens, qo_indptr, out, out_dtype)
+    types = (torch.int32, getattr(torch, "uint32", torch.int32))
+    m = _arg(fn, "tree_mask", tree_mask, types, (q.shape[0], (geom.qo_len + 31) // 32))
+    _check(fn, load().trtv_verify_tree(*a, m, o, out_dtype, _ws_arg(fn, workspace, ws_bytes), ws_bytes, _stream(stream)))
+
+
+def trtv_tree_commit(geom: Geom, kv_pool, page_table, kv_lens, qo_indptr, path, path_len, new_kv_lens,
+                     stream=None) -> None:
+    """Accepted path's cache rows to the front of the tree's positions, and the new lengths."""
+    import torch
+    fn = "trtv_tree_commit"
+    pt, kl, ip = _tables(fn, geom, page_table, kv_lens, qo_indptr)
+    _check(fn, load().trtv_tree_commit(
+        ctypes.byref(geom), _pool_arg(fn, geom, kv_pool), pt, kl, ip,
+        _arg(fn, "path", path, torch.int32, (geom.batch, None)),
+        _arg(fn, "path_len", path_len, torch.int32, (geom.batch,)), path.shape[1],
+        _arg(fn, "new_kv_lens", new_kv_lens, torch.int32, (geom.batch,)), _stream(stream)))

@@ -13,6 +13,7 @@
 #include <utility>
 
 #include "common.cuh"
+#include "host.h"
 #include "launch.h"
 
 // Per-device error word (TRTV_DEVERR_* bits), set by the kernels.
@@ -27,8 +28,6 @@ namespace trtv {
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr size_t kSmemOptin = 232448;  // opt-in shared memory per block on sm_103
-constexpr size_t kAlignSlack = 1024;
 
 std::mutex g_mu;
 int g_sm_count[kMaxDevices];
@@ -45,6 +44,8 @@ int current_device() {
   if (cudaGetDevice(&d) != cudaSuccess || d < 0 || d >= kMaxDevices) return -1;
   return d;
 }
+
+}  // namespace
 
 int sm_count() {
   const int d = current_device();
@@ -70,6 +71,8 @@ int* err_word() {
   return g_err_ptr[d];
 }
 
+namespace {
+
 // Device address of g_noalloc_scratch on the current device.  The host-side
 // name of the array is only a stand-in: the address comes from
 // cudaGetSymbolAddress, once per device, with that device current.
@@ -85,6 +88,8 @@ uint8_t* noalloc_scratch() {
   return g_noalloc_ptr[d];
 }
 
+}  // namespace
+
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   std::lock_guard<std::mutex> lk(g_mu);
   if (g_encode == nullptr) {
@@ -99,15 +104,16 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   return g_encode;
 }
 
+uint64_t wait_limit_ns() { return g_wait_ns.load(); }
+int withheld_pages() { return g_withhold.load(); }
+
+namespace {
+
 int next_pow2(int x) {
   int p = 1;
   while (p < x) p <<= 1;
   return p;
 }
-
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 // Derived shape of one call.
 struct Plan {
@@ -530,8 +536,8 @@ trtv_status attn_common(const trtv_geom* g, const void* q, const void* pool, con
   a.setup = pm ? kPmSeqSetup : umma ? kUmmaSeqSetup : kSeqSetup;
   a.lg_group = 0;
   while ((1 << a.lg_group) < pl.group) ++a.lg_group;
-  a.wait_ns = g_wait_ns.load();
-  a.withhold = g_withhold.load();
+  a.wait_ns = wait_limit_ns();
+  a.withhold = withheld_pages();
   cudaError_t e;
   if (rebuilt != nullptr) {
     e = launch_flat_table(false, kvi.flat, lens, g->batch, g->qo_len, g->max_pages_per_req, rebuilt,
@@ -706,8 +712,8 @@ trtv_status proxy_common(const trtv_geom* g, const void* q, const void* kv_pool,
   a.rows_pad = pl.rows_pad;
   a.num_ctas = pl.num_ctas;
   a.score_scale = g->sm_scale * g->k_scale;
-  a.wait_ns = g_wait_ns.load();
-  a.withhold = g_withhold.load();
+  a.wait_ns = wait_limit_ns();
+  a.withhold = withheld_pages();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool fused = select && umma;
   if (fused) {

@@ -1,0 +1,185 @@
+// abi_rows.cu -- the C ABI's packed-row calls (include/trtv.h): staging with
+// norm and rotation, prompt attention, tree attention and tree commit.  Host
+// code only: argument checks and launches; nothing is allocated, synchronised
+// or read from the device, so every call can be captured into a CUDA graph.
+#include <algorithm>
+#include <cmath>
+
+#include "host.h"
+#include "launch.h"
+#include "rows.cuh"
+
+namespace trtv {
+namespace {
+
+constexpr int kMaxBatch = 4096;
+constexpr int kMaxTreeTokens = 128;
+
+// Geometry checks shared by the packed-row calls.
+trtv_status rows_geom(const trtv_geom* g, const int32_t* indptr, int32_t num_tokens, RowsGeom* r) {
+  if (g == nullptr) return TRTV_ERR_INVALID_ARG;
+  if (g->batch < 1 || g->qo_len < 1 || g->num_q_heads < 1 || g->num_kv_heads < 1 ||
+      g->num_q_heads % g->num_kv_heads != 0 || g->max_pages_per_req < 1 || g->num_slots < 1 || g->slot_stride < 2 ||
+      g->num_ctas < 0 || g->num_ctas > kMaxCombineParts)
+    return TRTV_ERR_INVALID_ARG;
+  if (g->kv_dtype != TRTV_BF16 && g->kv_dtype != TRTV_FP8_E4M3) return TRTV_ERR_INVALID_ARG;
+  if (!(g->sm_scale > 0.f) || !(g->k_scale > 0.f) || !std::isfinite(g->sm_scale) || !std::isfinite(g->k_scale) ||
+      !std::isfinite(g->v_scale))
+    return TRTV_ERR_INVALID_ARG;
+  if (g->head_dim != 64 && g->head_dim != 128) return TRTV_ERR_UNSUPPORTED;
+  if (g->kv_dtype == TRTV_FP8_E4M3 && g->head_dim != 128) return TRTV_ERR_UNSUPPORTED;
+  if (g->batch > kMaxBatch || g->num_q_heads / g->num_kv_heads > 128) return TRTV_ERR_UNSUPPORTED;
+  // cache positions are 32-bit, and the pool is addressed by 32-bit rows
+  if (g->max_pages_per_req > (1 << 23)) return TRTV_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(g->num_slots) * g->slot_stride * kGroups * g->num_kv_heads * kSub >= (int64_t{1} << 31))
+    return TRTV_ERR_UNSUPPORTED;
+  if (num_tokens < 0) return TRTV_ERR_INVALID_ARG;
+  if (indptr == nullptr && static_cast<int64_t>(g->batch) * g->qo_len > num_tokens) return TRTV_ERR_INVALID_ARG;
+  if (!aligned(indptr, 4)) return TRTV_ERR_INVALID_ARG;
+  r->indptr = indptr;
+  r->batch = g->batch;
+  r->qo_len = g->qo_len;
+  r->num_tokens = num_tokens;
+  r->num_q_heads = g->num_q_heads;
+  r->num_kv_heads = g->num_kv_heads;
+  r->group = g->num_q_heads / g->num_kv_heads;
+  r->max_pages = g->max_pages_per_req;
+  r->num_slots = g->num_slots;
+  r->slot_stride = g->slot_stride;
+  return TRTV_OK;
+}
+
+trtv_status rows_device(RowsGeom* r, const int32_t* page_table, const int32_t* kv_lens) {
+  if (page_table == nullptr || kv_lens == nullptr || !aligned(page_table, 4) || !aligned(kv_lens, 4))
+    return TRTV_ERR_INVALID_ARG;
+  r->page_table = page_table;
+  r->kv_lens = kv_lens;
+  r->err = err_word();
+  return r->err == nullptr ? TRTV_ERR_CUDA : TRTV_OK;
+}
+
+trtv_status rows_attn(const trtv_geom* g, const void* q, const void* pool, const int32_t* page_table,
+                      const int32_t* kv_lens, const int32_t* indptr, int32_t num_tokens, const uint32_t* mask,
+                      void* out, int32_t out_dtype, void* ws, size_t ws_bytes, void* stream) {
+  RowsAttnParams p{};
+  trtv_status s = rows_geom(g, indptr, num_tokens, &p.g);
+  if (s != TRTV_OK || num_tokens == 0) return s;
+  if (q == nullptr || pool == nullptr || out == nullptr) return TRTV_ERR_INVALID_ARG;
+  if (out_dtype != TRTV_BF16 && out_dtype != TRTV_F32) return TRTV_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 16) || !aligned(mask, 4)) return TRTV_ERR_INVALID_ARG;
+  if (ws == nullptr || !aligned(ws, 256) || ws_bytes < trtv_workspace_bytes_rows(g)) return TRTV_ERR_WORKSPACE;
+  if ((s = rows_device(&p.g, page_table, kv_lens)) != TRTV_OK) return s;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.tree_mask = mask;
+  p.mask_words = (g->qo_len + 31) / 32;
+  p.out = out;
+  p.pool = pool;
+  p.out_f32 = out_dtype == TRTV_F32;
+  p.scale_log2 = g->sm_scale * g->k_scale * 1.4426950408889634f;
+  p.v_scale = g->v_scale;
+  const cudaError_t e = launch_rows_attn(g->head_dim, g->kv_dtype == TRTV_FP8_E4M3, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TRTV_OK : TRTV_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace trtv
+
+using namespace trtv;
+
+extern "C" {
+
+trtv_status trtv_norm_rope_stage(const trtv_geom* g, const trtv_norm_rope* in, const int32_t* qo_indptr,
+                                 int32_t num_tokens, void* q_out, void* kv_pool, const int32_t* page_table,
+                                 const int32_t* kv_lens, void* stream) {
+  NormRopeParams p{};
+  trtv_status s = rows_geom(g, qo_indptr, num_tokens, &p.g);
+  if (s != TRTV_OK || num_tokens == 0) return s;
+  if (in == nullptr || in->q == nullptr || in->k == nullptr || in->v == nullptr || q_out == nullptr ||
+      kv_pool == nullptr)
+    return TRTV_ERR_INVALID_ARG;
+  const int D = g->head_dim;
+  const int64_t qw = static_cast<int64_t>(g->num_q_heads) * D, kw = static_cast<int64_t>(g->num_kv_heads) * D;
+  if (in->q_stride < qw || in->k_stride < kw || in->v_stride < kw || in->q_stride % 8 || in->k_stride % 8 ||
+      in->v_stride % 8)
+    return TRTV_ERR_INVALID_ARG;
+  if (in->rot_dim < 0 || in->rot_dim > D || in->rot_dim % 8 != 0 || (in->interleaved != 0 && in->interleaved != 1) ||
+      !(in->eps >= 0.f) || !std::isfinite(in->eps))
+    return TRTV_ERR_INVALID_ARG;
+  if (in->rot_dim > 0 && (in->rope_table == nullptr || in->table_len < 1)) return TRTV_ERR_INVALID_ARG;
+  if (in->q == q_out && in->q_stride != qw) return TRTV_ERR_INVALID_ARG;
+  const void* ptrs[] = {in->q, in->k, in->v, in->q_weight, in->k_weight, in->rope_table, q_out, kv_pool};
+  for (const void* x : ptrs)
+    if (!aligned(x, 16)) return TRTV_ERR_INVALID_ARG;
+  if (!aligned(in->positions, 4)) return TRTV_ERR_INVALID_ARG;
+  const int heads = g->num_q_heads + 2 * g->num_kv_heads;
+  if (static_cast<int64_t>(num_tokens) * heads >= (int64_t{1} << 33)) return TRTV_ERR_UNSUPPORTED;  // grid size
+  if ((s = rows_device(&p.g, page_table, kv_lens)) != TRTV_OK) return s;
+  p.q = static_cast<const __nv_bfloat16*>(in->q);
+  p.k = static_cast<const __nv_bfloat16*>(in->k);
+  p.v = static_cast<const __nv_bfloat16*>(in->v);
+  p.q_stride = in->q_stride;
+  p.k_stride = in->k_stride;
+  p.v_stride = in->v_stride;
+  p.q_weight = static_cast<const __nv_bfloat16*>(in->q_weight);
+  p.k_weight = static_cast<const __nv_bfloat16*>(in->k_weight);
+  p.rope = in->rope_table;
+  p.positions = in->positions;
+  p.q_out = static_cast<__nv_bfloat16*>(q_out);
+  p.pool = kv_pool;
+  p.table_len = in->table_len;
+  p.rot_dim = in->rot_dim;
+  p.interleaved = in->interleaved;
+  p.eps = in->eps;
+  p.k_scale = g->k_scale;
+  p.v_scale = g->v_scale;
+  p.heads_per_warp = 4 * (256 / D);  // one batch of rows in flight
+  const cudaError_t e = launch_norm_rope_stage(D, g->kv_dtype == TRTV_FP8_E4M3, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TRTV_OK : TRTV_ERR_CUDA;
+}
+
+size_t trtv_workspace_bytes_rows(const trtv_geom* geom) {
+  RowsGeom r{};
+  if (rows_geom(geom, nullptr, 0x7fffffff, &r) != TRTV_OK) return 0;
+  return 256;
+}
+
+trtv_status trtv_prompt_attn(const trtv_geom* g, const void* q, const void* kv_pool, const int32_t* page_table,
+                             const int32_t* kv_lens, const int32_t* qo_indptr, int32_t num_tokens, void* out,
+                             int32_t out_dtype, void* workspace, size_t ws_bytes, void* stream) {
+  return rows_attn(g, q, kv_pool, page_table, kv_lens, qo_indptr, num_tokens, nullptr, out, out_dtype, workspace,
+                   ws_bytes, stream);
+}
+
+trtv_status trtv_verify_tree(const trtv_geom* g, const void* q, const void* kv_pool, const int32_t* page_table,
+                             const int32_t* kv_lens, const int32_t* qo_indptr, int32_t num_tokens,
+                             const uint32_t* tree_mask, void* out, int32_t out_dtype, void* workspace,
+                             size_t ws_bytes, void* stream) {
+  if (tree_mask == nullptr) return TRTV_ERR_INVALID_ARG;
+  if (g != nullptr && g->qo_len > kMaxTreeTokens) return TRTV_ERR_UNSUPPORTED;
+  return rows_attn(g, q, kv_pool, page_table, kv_lens, qo_indptr, num_tokens, tree_mask, out, out_dtype, workspace,
+                   ws_bytes, stream);
+}
+
+trtv_status trtv_tree_commit(const trtv_geom* g, void* kv_pool, const int32_t* page_table, const int32_t* kv_lens,
+                             const int32_t* qo_indptr, const int32_t* path, const int32_t* path_len,
+                             int32_t max_path, int32_t* new_kv_lens, void* stream) {
+  CommitParams p{};
+  trtv_status s = rows_geom(g, qo_indptr, 0x7fffffff, &p.g);  // no row-indexed buffer here
+  if (s != TRTV_OK) return s;
+  if (kv_pool == nullptr || path == nullptr || path_len == nullptr || new_kv_lens == nullptr || max_path < 1)
+    return TRTV_ERR_INVALID_ARG;
+  if (!aligned(kv_pool, 16) || !aligned(path, 4) || !aligned(path_len, 4) || !aligned(new_kv_lens, 4))
+    return TRTV_ERR_INVALID_ARG;
+  if (g->qo_len > kMaxTreeTokens) return TRTV_ERR_UNSUPPORTED;
+  if ((s = rows_device(&p.g, page_table, kv_lens)) != TRTV_OK) return s;
+  p.pool = static_cast<uint8_t*>(kv_pool);
+  p.path = path;
+  p.path_len = path_len;
+  p.new_kv_lens = new_kv_lens;
+  p.max_path = max_path;
+  p.row_bytes = g->head_dim * (g->kv_dtype == TRTV_FP8_E4M3 ? 1 : 2);
+  const cudaError_t e = launch_tree_commit(p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TRTV_OK : TRTV_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,105 @@
+// rows.cuh -- packed token rows (qo_indptr): which rows a request owns, and
+// the launch parameters of the calls that take them.
+#pragma once
+
+#include "common.cuh"
+
+namespace trtv {
+
+struct RowsGeom {
+  const int32_t* indptr;   // [batch + 1] or null: qo_len rows per request
+  const int32_t* kv_lens;
+  const int32_t* page_table;
+  int* err;
+  int batch, qo_len, num_tokens;
+  int num_q_heads, num_kv_heads, group;
+  int max_pages, num_slots, slot_stride;
+};
+
+// Rows row0 .. row0 + n - 1 of request b; n = 0 when it has none, or when its
+// qo_indptr entries do not fit (ok = false).
+struct RowSpan {
+  int row0, n;
+  bool ok;
+};
+
+__device__ __forceinline__ RowSpan row_span(const RowsGeom& g, int b) {
+  if (g.indptr == nullptr) return {b * g.qo_len, g.qo_len, true};
+  const int lo = g.indptr[b], hi = g.indptr[b + 1];
+  // hi - lo cannot overflow once both lie in [0, num_tokens]
+  if (lo < 0 || hi > g.num_tokens || lo > hi || hi - lo > g.qo_len || (b == 0 && lo != 0)) return {0, 0, false};
+  return {lo, hi - lo, true};
+}
+
+// Flags qo_indptr entries that do not fit; every thread of one CTA calls it.
+__device__ __forceinline__ void check_spans(const RowsGeom& g) {
+  if (g.indptr == nullptr) return;
+  for (int b = threadIdx.x; b < g.batch; b += blockDim.x)
+    if (!row_span(g, b).ok) atomicOr(g.err, TRTV_DEVERR_INDPTR);
+}
+
+// The request whose rows hold `row` (the last b with indptr[b] <= row); the
+// whole warp calls it with one row.  32-ary search: one coalesced-ish load
+// round per factor of 32 in the batch.
+__device__ __forceinline__ int row_request(const RowsGeom& g, int row, int lane) {
+  if (g.indptr == nullptr) return row / g.qo_len;
+  int lo = 0, hi = g.batch;
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int i = lo + lane * step;
+    const unsigned m = __ballot_sync(0xffffffffu, i < hi && g.indptr[i] <= row);
+    const int k = m == 0 ? 0 : 31 - __clz(m);
+    lo += k * step;
+    hi = min(hi, lo + step);
+  }
+  return lo;
+}
+
+// Element offset, inside the pool, of cache position `pos`'s row of KV head 0
+// in slot s's K page (V: one buffer further).
+__device__ __forceinline__ int64_t cell_offset(const RowsGeom& g, int64_t s, int pos, int D) {
+  return (s * g.slot_stride * kGroups + (pos % kPage) / kSub) * g.num_kv_heads * static_cast<int64_t>(kSub) * D +
+         static_cast<int64_t>(pos % kSub) * D;
+}
+
+struct NormRopeParams {
+  RowsGeom g;
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const __nv_bfloat16* v;
+  int64_t q_stride, k_stride, v_stride;
+  const __nv_bfloat16* q_weight;
+  const __nv_bfloat16* k_weight;
+  const float* rope;
+  const int32_t* positions;
+  __nv_bfloat16* q_out;
+  void* pool;
+  int table_len, rot_dim, interleaved;
+  int heads_per_warp;   // heads of a token that one warp takes
+  float eps, k_scale, v_scale;
+};
+
+struct CommitParams {
+  RowsGeom g;
+  uint8_t* pool;
+  const int32_t* path;
+  const int32_t* path_len;
+  int32_t* new_kv_lens;
+  int max_path, row_bytes;  // bytes of one head's row in the cache
+};
+
+struct RowsAttnParams {
+  RowsGeom g;
+  const __nv_bfloat16* q;
+  const uint32_t* tree_mask;   // [num_tokens, mask_words] or null: the causal bound
+  void* out;
+  const void* pool;
+  int mask_words, out_f32;
+  float scale_log2, v_scale;   // sm_scale * k_scale * log2(e)
+};
+
+cudaError_t launch_rows_attn(int head_dim, bool fp8, const RowsAttnParams& p, cudaStream_t st);
+cudaError_t launch_norm_rope_stage(int head_dim, bool fp8, const NormRopeParams& p, cudaStream_t st);
+cudaError_t launch_tree_commit(const CommitParams& p, cudaStream_t st);
+
+}  // namespace trtv

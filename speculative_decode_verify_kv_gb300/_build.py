@@ -19,7 +19,8 @@ LIB = os.path.join(LIBDIR, "libtrtv.so")
 ROOT = os.path.dirname(HERE)
 
 SOURCES = ["abi.cu", "small_kernels.cu", "attn_bf16.cu", "attn_fp8.cu", "attn_pm.cu", "proxy_bf16.cu",
-           "proxy_fp8.cu", "abi_rows.cu", "row_kernels.cu", "rows_attn.cu"]
+           "proxy_fp8.cu", "abi_rows.cu", "row_kernels.cu", "rows_attn_bf16.cu",
+           "rows_attn_fp8.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
          "-I" + os.path.join(ROOT, "include")]

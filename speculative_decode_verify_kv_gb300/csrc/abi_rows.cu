@@ -14,6 +14,7 @@ namespace {
 
 constexpr int kMaxBatch = 4096;
 constexpr int kMaxTreeTokens = 128;
+constexpr int kRowsSetup = 128;  // stream-K charge of an item, in positions
 
 // Geometry checks shared by the packed-row calls.
 trtv_status rows_geom(const trtv_geom* g, const int32_t* indptr, int32_t num_tokens, RowsGeom* r) {
@@ -58,6 +59,93 @@ trtv_status rows_device(RowsGeom* r, const int32_t* page_table, const int32_t* k
   return r->err == nullptr ? TRTV_ERR_CUDA : TRTV_OK;
 }
 
+// What one attention call needs besides its pointers.
+struct RowsPlan {
+  bool two;            // 256-row items
+  int num_ctas;
+  size_t ws_o, ws_lse, ws_splits, ws_total;
+};
+
+// 256-row items where a request can fill more than one 128-row tile: its tiles
+// share each page's bytes and the two softmax groups have a tile each.
+// Otherwise the groups take a tile's pages in turn.
+bool rows_plan(const trtv_geom* g, const RowsGeom& r, RowsPlan* pl) {
+  const int tile_toks = kRowsTile / r.group;
+  pl->two = g->qo_len > tile_toks;
+  pl->num_ctas = g->num_ctas > 0 ? g->num_ctas : sm_count();
+  if (pl->num_ctas <= 0) return false;
+  const size_t rows = pl->two ? 2 * kRowsTile : kRowsTile, pieces = 2 * static_cast<size_t>(pl->num_ctas);
+  size_t off = 0;
+  pl->ws_o = off;
+  off = align_up(off + pieces * rows * g->head_dim * sizeof(float), 256);
+  pl->ws_lse = off;
+  off = align_up(off + pieces * rows * sizeof(float), 256);
+  pl->ws_splits = off;
+  off = align_up(off + pl->num_ctas * sizeof(RowsSplit), 256);
+  pl->ws_total = off;
+  return true;
+}
+
+// Shared memory: Q (two tiles), the page ring, E4M3: the codes' ring, the
+// groups' exchange, the requests' scan, barriers.  The ring takes what is left,
+// at most kMaxStages pages.
+constexpr int kMaxStages = 8;
+bool rows_smem(const trtv_geom* g, const RowsPlan& pl, RowsAttnParams* p, size_t* bytes) {
+  const bool fp8 = g->kv_dtype == TRTV_FP8_E4M3;
+  const size_t tile = static_cast<size_t>(kRowsTile) * g->head_dim * 2, raw = static_cast<size_t>(kRowsTile) * g->head_dim;
+  const size_t scan = align_up((static_cast<size_t>(g->batch) + 1 + 16) * sizeof(int64_t), 16);
+  const size_t ml = pl.two ? 0 : 2 * kRowsTile * 2 * sizeof(float);
+  const size_t bars = (4 * kMaxStages + 16) * sizeof(uint64_t);
+  const size_t fixed = 2 * tile + ml + scan + bars + kAlignSlack;
+  p->nraw = fp8 ? 3 : 0;
+  const size_t codes = p->nraw * raw;
+  if (fixed + codes + 3 * tile > kSmemOptin) return false;
+  p->nst = static_cast<int>(std::min<size_t>((kSmemOptin - fixed - codes) / tile, kMaxStages));
+  size_t off = 0;
+  p->off_q = 0;
+  off += 2 * tile;
+  p->off_ring = static_cast<int>(off);
+  off += p->nst * tile;
+  p->off_raw = static_cast<int>(off);
+  off += codes;
+  p->off_ml = static_cast<int>(off);
+  off += ml;
+  p->off_scan = static_cast<int>(off);
+  off += scan;
+  p->off_bar = static_cast<int>(off);
+  off += bars;
+  *bytes = off + kAlignSlack;
+  return true;
+}
+
+// The pool as [sub-pages][KV heads][32 rows][head_dim]: a box is one head's
+// 128-byte column block of a whole page.
+bool encode_pages(const trtv_geom* g, const void* pool, CUtensorMap* map) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+  if (enc == nullptr) return false;
+  const bool fp8 = g->kv_dtype == TRTV_FP8_E4M3;
+  const cuuint64_t elem = fp8 ? 1 : 2, D = g->head_dim, Hk = g->num_kv_heads;
+  cuuint64_t dims[4] = {D, kSub, Hk, static_cast<cuuint64_t>(g->num_slots) * g->slot_stride * kGroups};
+  cuuint64_t strides[3] = {D * elem, kSub * D * elem, Hk * kSub * D * elem};
+  cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / elem), kSub, 1, kGroups}, estr[4] = {1, 1, 1, 1};
+  return enc(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(pool),
+             dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// q as [rows][query heads][head_dim]: a box is one tile's 64-column block (its
+// tokens' heads of one group).
+bool encode_rows(const trtv_geom* g, const RowsGeom& r, int tile_toks, const void* q, CUtensorMap* map) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t D = g->head_dim, Hq = g->num_q_heads;
+  cuuint64_t dims[3] = {D, Hq, static_cast<cuuint64_t>(r.num_tokens)}, strides[2] = {D * 2, Hq * D * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(r.group), static_cast<cuuint32_t>(tile_toks)}, estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 trtv_status rows_attn(const trtv_geom* g, const void* q, const void* pool, const int32_t* page_table,
                       const int32_t* kv_lens, const int32_t* indptr, int32_t num_tokens, const uint32_t* mask,
                       void* out, int32_t out_dtype, void* ws, size_t ws_bytes, void* stream) {
@@ -67,17 +155,35 @@ trtv_status rows_attn(const trtv_geom* g, const void* q, const void* pool, const
   if (q == nullptr || pool == nullptr || out == nullptr) return TRTV_ERR_INVALID_ARG;
   if (out_dtype != TRTV_BF16 && out_dtype != TRTV_F32) return TRTV_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(pool, 16) || !aligned(out, 16) || !aligned(mask, 4)) return TRTV_ERR_INVALID_ARG;
-  if (ws == nullptr || !aligned(ws, 256) || ws_bytes < trtv_workspace_bytes_rows(g)) return TRTV_ERR_WORKSPACE;
+  if (page_table == nullptr || kv_lens == nullptr || !aligned(page_table, 4) || !aligned(kv_lens, 4))
+    return TRTV_ERR_INVALID_ARG;
+  RowsPlan pl;
+  if (!rows_plan(g, p.g, &pl)) return TRTV_ERR_CUDA;
+  if (ws == nullptr || !aligned(ws, 256) || ws_bytes < pl.ws_total) return TRTV_ERR_WORKSPACE;
+  size_t smem = 0;
+  if (!rows_smem(g, pl, &p, &smem)) return TRTV_ERR_UNSUPPORTED;
   if ((s = rows_device(&p.g, page_table, kv_lens)) != TRTV_OK) return s;
-  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.tile_toks = kRowsTile / p.g.group;
+  CUtensorMap kv_map, q_map;
+  if (!encode_pages(g, pool, &kv_map) || !encode_rows(g, p.g, p.tile_toks, q, &q_map)) return TRTV_ERR_CUDA;
+  uint8_t* wsb = static_cast<uint8_t*>(ws);
   p.tree_mask = mask;
   p.mask_words = (g->qo_len + 31) / 32;
   p.out = out;
-  p.pool = pool;
+  p.ws_o = reinterpret_cast<float*>(wsb + pl.ws_o);
+  p.ws_lse = reinterpret_cast<float*>(wsb + pl.ws_lse);
+  p.splits = reinterpret_cast<RowsSplit*>(wsb + pl.ws_splits);
   p.out_f32 = out_dtype == TRTV_F32;
+  p.num_ctas = pl.num_ctas;
+  p.setup = kRowsSetup;
   p.scale_log2 = g->sm_scale * g->k_scale * 1.4426950408889634f;
   p.v_scale = g->v_scale;
-  const cudaError_t e = launch_rows_attn(g->head_dim, g->kv_dtype == TRTV_FP8_E4M3, p, static_cast<cudaStream_t>(stream));
+  p.wait_ns = wait_limit_ns();
+  p.withhold = withheld_pages();
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = g->kv_dtype == TRTV_FP8_E4M3 ? launch_rows_attn_fp8(pl.two, kv_map, q_map, p, smem, st)
+                                               : launch_rows_attn_bf16(g->head_dim, pl.two, kv_map, q_map, p, smem, st);
+  if (e == cudaSuccess) e = launch_rows_join(g->head_dim, pl.two, p, st);
   return e == cudaSuccess ? TRTV_OK : TRTV_ERR_CUDA;
 }
 
@@ -139,8 +245,12 @@ trtv_status trtv_norm_rope_stage(const trtv_geom* g, const trtv_norm_rope* in, c
 
 size_t trtv_workspace_bytes_rows(const trtv_geom* geom) {
   RowsGeom r{};
-  if (rows_geom(geom, nullptr, 0x7fffffff, &r) != TRTV_OK) return 0;
-  return 256;
+  RowsPlan pl;
+  RowsAttnParams p{};
+  size_t smem = 0;
+  const int32_t any = 0;  // (rows are not checked: a host pointer that nothing reads)
+  if (rows_geom(geom, &any, 0, &r) != TRTV_OK || !rows_plan(geom, r, &pl) || !rows_smem(geom, pl, &p, &smem)) return 0;
+  return pl.ws_total;
 }
 
 trtv_status trtv_prompt_attn(const trtv_geom* g, const void* q, const void* kv_pool, const int32_t* page_table,

@@ -88,17 +88,40 @@ struct CommitParams {
   int max_path, row_bytes;  // bytes of one head's row in the cache
 };
 
-struct RowsAttnParams {
-  RowsGeom g;
-  const __nv_bfloat16* q;
-  const uint32_t* tree_mask;   // [num_tokens, mask_words] or null: the causal bound
-  void* out;
-  const void* pool;
-  int mask_words, out_f32;
-  float scale_log2, v_scale;   // sm_scale * k_scale * log2(e)
+constexpr int kRowsTile = 128;   // rows of one UMMA tile of the attention
+
+// A row-tile item of the attention that the stream-K split cut: written by the
+// CTA that holds its first page, read by the join kernel.
+struct RowsSplit {
+  int b, h, tok0, n, row0, c_last;  // b < 0: none.  tok0: the item's first token of the request
+  int pages, pad;
+  long long first, W;               // unit of its first page; units of the call
 };
 
-cudaError_t launch_rows_attn(int head_dim, bool fp8, const RowsAttnParams& p, cudaStream_t st);
+struct RowsAttnParams {
+  RowsGeom g;
+  const uint32_t* tree_mask;   // [num_tokens, mask_words] or null: the causal bound
+  void* out;
+  float* ws_o;                 // [2 * num_ctas, rows, D] pieces, each normalised by its own sum
+  float* ws_lse;               // [2 * num_ctas, rows] log2 of their sums
+  RowsSplit* splits;           // [num_ctas]
+  int mask_words, out_f32, num_ctas;
+  int tile_toks;               // tokens of a 128-row tile: 128 / group
+  int nst, nraw;               // page stages in shared memory; FP8: stages of raw codes
+  int off_q, off_ring, off_raw, off_ml, off_scan, off_bar;   // shared memory, from the 1024-aligned base
+  int setup;                   // what starting an item costs, in positions
+  float scale_log2, v_scale;   // sm_scale * k_scale * log2(e)
+  uint64_t wait_ns;
+  int withhold;
+};
+
+// two: 256 rows (two tiles) per item, else 128 rows whose pages two softmax
+// groups take in turn
+cudaError_t launch_rows_attn_bf16(int head_dim, bool two, const CUtensorMap& kv_map, const CUtensorMap& q_map,
+                                  const RowsAttnParams& p, size_t smem, cudaStream_t st);
+cudaError_t launch_rows_attn_fp8(bool two, const CUtensorMap& kv_map, const CUtensorMap& q_map,
+                                 const RowsAttnParams& p, size_t smem, cudaStream_t st);
+cudaError_t launch_rows_join(int head_dim, bool two, const RowsAttnParams& p, cudaStream_t st);
 cudaError_t launch_norm_rope_stage(int head_dim, bool fp8, const NormRopeParams& p, cudaStream_t st);
 cudaError_t launch_tree_commit(const CommitParams& p, cudaStream_t st);
 

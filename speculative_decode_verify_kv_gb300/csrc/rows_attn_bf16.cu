@@ -1,0 +1,16 @@
+// rows_attn_bf16.cu -- prompt and tree attention over bf16 caches.
+#include "launch.h"
+#include "rows_attn.cuh"
+
+namespace trtv {
+
+cudaError_t launch_rows_attn_bf16(int head_dim, bool two, const CUtensorMap& kv_map, const CUtensorMap& q_map,
+                                  const RowsAttnParams& p, size_t smem, cudaStream_t st) {
+  if (head_dim == 64)
+    return two ? launch_rows_attn_one<64, false, true>(kv_map, q_map, p, smem, st)
+               : launch_rows_attn_one<64, false, false>(kv_map, q_map, p, smem, st);
+  return two ? launch_rows_attn_one<128, false, true>(kv_map, q_map, p, smem, st)
+             : launch_rows_attn_one<128, false, false>(kv_map, q_map, p, smem, st);
+}
+
+}  // namespace trtv

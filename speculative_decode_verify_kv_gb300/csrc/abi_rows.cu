@@ -12,7 +12,7 @@
 namespace trtv {
 namespace {
 
-constexpr int kMaxBatch = 4096;
+constexpr int kMaxBatch = 2048;   // the requests' scan lies in shared memory
 constexpr int kMaxTreeTokens = 128;
 constexpr int kRowsSetup = 128;  // stream-K charge of an item, in positions
 
@@ -87,17 +87,20 @@ bool rows_plan(const trtv_geom* g, const RowsGeom& r, RowsPlan* pl) {
 }
 
 // Shared memory: Q (two tiles), the page ring, E4M3: the codes' ring, the
-// groups' exchange, the requests' scan, barriers.  The ring takes what is left,
+// groups' exchange, the output rows' staging, the
+// pieces, the requests' scan and its 32 warp totals, barriers.  The ring takes what is left,
 // at most kMaxStages pages.
 constexpr int kMaxStages = 8;
 bool rows_smem(const trtv_geom* g, const RowsPlan& pl, RowsAttnParams* p, size_t* bytes) {
   const bool fp8 = g->kv_dtype == TRTV_FP8_E4M3;
   const size_t tile = static_cast<size_t>(kRowsTile) * g->head_dim * 2, raw = static_cast<size_t>(kRowsTile) * g->head_dim;
-  const size_t scan = align_up((static_cast<size_t>(g->batch) + 1 + 16) * sizeof(int64_t), 16);
+  const size_t scan = align_up((static_cast<size_t>(g->batch) + 1 + 32) * sizeof(int64_t), 16);
   const size_t ml = pl.two ? 0 : 2 * kRowsTile * 2 * sizeof(float);
-  const size_t bars = (4 * kMaxStages + 16) * sizeof(uint64_t);
-  const size_t fixed = 2 * tile + ml + scan + bars + kAlignSlack;
-  p->nraw = fp8 ? 3 : 0;
+  const size_t bars = (4 * kMaxStages + 32) * sizeof(uint64_t), pieces = 4 * 64;
+  const size_t stage = static_cast<size_t>(8) * 32 * rows_segment(fp8);
+  const size_t fixed = 2 * tile + ml + stage + pieces + scan + bars + kAlignSlack;
+  // two stages of codes at least, a third where the requests' scan leaves room
+  p->nraw = !fp8 ? 0 : fixed + 3 * raw + 3 * tile <= kSmemOptin ? 3 : 2;
   const size_t codes = p->nraw * raw;
   if (fixed + codes + 3 * tile > kSmemOptin) return false;
   p->nst = static_cast<int>(std::min<size_t>((kSmemOptin - fixed - codes) / tile, kMaxStages));
@@ -110,6 +113,10 @@ bool rows_smem(const trtv_geom* g, const RowsPlan& pl, RowsAttnParams* p, size_t
   off += codes;
   p->off_ml = static_cast<int>(off);
   off += ml;
+  p->off_stage = static_cast<int>(off);
+  off += stage;
+  p->off_pieces = static_cast<int>(off);
+  off += pieces;
   p->off_scan = static_cast<int>(off);
   off += scan;
   p->off_bar = static_cast<int>(off);

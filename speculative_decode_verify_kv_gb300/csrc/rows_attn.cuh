@@ -30,9 +30,16 @@
 // (exact for elements within 2^-29 of the row's largest), undone in the logits'
 // scale.
 //
-// Warps: 0-3 and 4-7 softmax groups, 8 page loads, 9 UMMA issue, 10 V pages'
-// relay (rows at or past kv_len are zeroed: P is zero there but 0 * NaN is
-// not), 11 Q loads, 12-15 (E4M3) conversion.
+// What bounds a prompt's page is one group's chain: softmax, then PV and the
+// next QK, which cannot start before P is written over S.  So a row's scores are
+// read from TMEM twice (a read of 32 columns takes 35 cycles, spilt registers
+// much more), and P is handed over in two halves, the first half's PV running
+// under the second half's exponentials.
+//
+// Warps: 0-3 and 4-7 softmax groups, 8 page loads, 9 (TWO: and 10) UMMA issue
+// (V rows at or past kv_len are zeroed first: P is zero there but 0 * NaN
+// is not), 11 the CTA's schedule (its pieces, a few ahead, in shared memory) and
+// Q loads, 12-15 (E4M3) conversion.
 #pragma once
 
 #include "rows.cuh"
@@ -122,6 +129,17 @@ struct RowsWalk {
   }
 };
 
+// One piece of an item, as the scheduling warp hands it to the others: the
+// item's place and the pages [j0, j1) of this CTA (e0, e1: where each softmax
+// group's pages end); j1 = 0 ends the CTA's work.
+struct __align__(16) RowsPiece {
+  int row0, tok0, n, ctx;   // the request's first row, the item's first token, the request's tokens, positions before them
+  int j0, j1, e0, e1;
+  int np, h, b, pad;        // the item's pages
+  int64_t first, pad2;      // unit of its first page
+};
+constexpr int kRowsPieces = 4;   // pieces scheduled ahead
+
 // Units of request b over all its items; 0 when it has none or is left out.
 __device__ __forceinline__ int64_t rows_units(const RowsAttnParams& p, int b, int toks, bool causal, bool flag) {
   const RowSpan s = row_span(p.g, b);
@@ -196,9 +214,52 @@ __device__ __forceinline__ void tma_load_q(void* dst, const CUtensorMap* map, ui
       : "memory");
 }
 
+// The products of one page and tile, issued by one elected lane (the whole warp
+// executes the call): one asm block, only the low word of a descriptor moves.
+//   S = Q K^T: HB x 4 steps of 16 head dims, 32 bytes apart in a 64-column
+//   block, the blocks 16 KB apart
+#define TRTV_QK_STEP(OFF, P)                                                                         \
+  "add.u32 x, %1, " #OFF ";\n\tadd.u32 y, %2, " #OFF ";\n\tmov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t" \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, " #P ";\n\t"
+template <int HB>
+__device__ __forceinline__ void umma_qk(uint32_t d, uint32_t q, uint32_t k, uint32_t desc_hi, uint32_t idesc) {
+  if constexpr (HB == 2) {
+    asm volatile(
+        "{\n\t.reg .pred e, f, t;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 f, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        TRTV_QK_STEP(0, f) TRTV_QK_STEP(2, t) TRTV_QK_STEP(4, t) TRTV_QK_STEP(6, t)
+        TRTV_QK_STEP(1024, t) TRTV_QK_STEP(1026, t) TRTV_QK_STEP(1028, t) TRTV_QK_STEP(1030, t)
+        "}\n" ::"r"(d), "r"(q), "r"(k), "r"(idesc), "r"(desc_hi)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred e, f, t;\n\t.reg .b32 x, y;\n\t.reg .b64 a, b;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 f, 0, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+        TRTV_QK_STEP(0, f) TRTV_QK_STEP(2, t) TRTV_QK_STEP(4, t) TRTV_QK_STEP(6, t)
+        "}\n" ::"r"(d), "r"(q), "r"(k), "r"(idesc), "r"(desc_hi)
+        : "memory");
+  }
+}
+#undef TRTV_QK_STEP
+//   O (+)= P V for half a page: 4 steps of 16 positions, 8 TMEM columns of P
+//   and 2 KB of V apart
+#define TRTV_PV_STEP(AO, BO, P)                                                          \
+  "add.u32 x, %1, " #AO ";\n\tadd.u32 y, %2, " #BO ";\n\tmov.b64 b, {y, %5};\n\t"        \
+  "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, " #P ";\n\t"
+__device__ __forceinline__ void umma_pv(uint32_t d, uint32_t pt, uint32_t v, uint32_t desc_hi, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred e, f, t;\n\t.reg .b32 x, y;\n\t.reg .b64 b;\n\telect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      TRTV_PV_STEP(0, 0, f) TRTV_PV_STEP(8, 128, t) TRTV_PV_STEP(16, 256, t) TRTV_PV_STEP(24, 384, t)
+      "}\n" ::"r"(d), "r"(pt), "r"(v), "r"(idesc), "r"(accumulate), "r"(desc_hi)
+      : "memory");
+}
+#undef TRTV_PV_STEP
+
 // Allowed columns of a page for one row of a tree, as four words: positions
 // before the tree all, node i by bit i of m (bits at n and above cleared).
-// off = first position of the page minus the tree's first.
+// off = the first column's position minus the tree's first.
 __device__ __forceinline__ void tree_window(const uint32_t (&m)[4], int off, uint32_t (&w)[4]) {
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -219,6 +280,51 @@ __device__ __forceinline__ void tree_window(const uint32_t (&m)[4], int off, uin
     }
     w[k] = __funnelshift_r(lo, hi, o & 31);
   }
+}
+
+// The same for a causal bound: columns 0 .. last.
+__device__ __forceinline__ void row_window(int last, uint32_t (&w)[4]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int o = last - 32 * k;
+    w[k] = o >= 31 ? 0xffffffffu : o < 0 ? 0u : (2u << o) - 1u;
+  }
+}
+
+// Of 32 scores, those that the row does not see (bits of w not set) become
+// minus infinity.
+__device__ __forceinline__ void row_mask(uint32_t w, uint32_t (&x)[32]) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k) x[k] = (w >> k) & 1u ? x[k] : 0xff800000u;
+}
+
+__device__ __forceinline__ float row_max(const uint32_t (&x)[32]) {
+  float a = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])), b = fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3]));
+#pragma unroll
+  for (int k = 4; k < 32; k += 4) {
+    a = max3(a, __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+    b = max3(b, __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+  }
+  return fmaxf(a, b);
+}
+
+// Weights 2^(x scale + negm) of columns 32 c .. 32 c + 31, stored over the scores
+// as 16-bit pairs (column ts + i of P holds positions 2i and 2i + 1); their sum
+// is added to `sum`.
+template <bool F16>
+__device__ __forceinline__ void row_exp(uint32_t ts, int c, const uint32_t (&x)[32], float scale, float negm, float2& sum) {
+  const float2 sc2 = make_float2(scale, scale), ng2 = make_float2(negm, negm);
+  uint32_t o[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    float2 v = make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
+    v = __ffma2_rn(v, sc2, ng2);
+    v.x = fast_exp2(v.x);
+    v.y = fast_exp2(v.y);
+    sum = __fadd2_rn(sum, v);
+    o[k] = pack2<F16>(v.x, v.y);
+  }
+  tmem_st16(ts + 16 * c, o);
 }
 
 template <int D, bool FP8, bool TWO>
@@ -242,20 +348,24 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
   const int NST = p.nst, NRAW = p.nraw;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.off_bar);  // [NST] page ready for the UMMAs
   uint64_t* empty = full + NST;                                    // [NST] UMMAs done with it
-  uint64_t* raw = empty + NST;      // bf16: [NST] V page landed (its relay then fills `full`); E4M3: [NRAW] codes landed
-  uint64_t* rawfree = raw + (FP8 ? NRAW : NST);                    // E4M3: [NRAW] codes converted
-  uint64_t* sfull = rawfree + (FP8 ? NRAW : 0);                    // [2] S of group s written
-  uint64_t* pfull = sfull + 2;                                     // [2] P of group s written
-  uint64_t* odone = pfull + 2;                                     // [2] last PV of the piece retired
+  uint64_t* raw = empty + NST;                                     // E4M3: [NRAW] codes landed
+  uint64_t* rawfree = raw + NRAW;                                  // E4M3: [NRAW] codes converted
+  uint64_t* sfull = rawfree + NRAW;                                // [2] S of group s written
+  uint64_t* pfull = sfull + 2;                                     // [2][2] P of group s, half h of the page, written
+  uint64_t* odone = pfull + 4;                                     // [2] last PV of the piece retired
   uint64_t* qfull = odone + 2;                                     // [2] Q tile landed
   uint64_t* qempty = qfull + 2;                                    // [2] last QK that reads it retired
   uint64_t* qconv = qempty + 2;                                    // [2] E4M3: Q tile converted to f16
-  uint64_t* mdone = qconv + 2;
-  uint32_t* tslot = reinterpret_cast<uint32_t*>(mdone + 1);
-  int* abortf = reinterpret_cast<int*>(mdone + 2);
+  uint64_t* ifull = qconv + 2;                                     // [kRowsPieces] piece scheduled
+  uint64_t* iempty = ifull + kRowsPieces;                          // [kRowsPieces] every role has copied it
+  uint64_t* turn = iempty + kRowsPieces;                           // [2] TWO: group s may issue
+  uint64_t* mdone = turn + 2;                                      // [2] an issuer's last UMMA retired
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(mdone + 2);
+  int* abortf = reinterpret_cast<int*>(mdone + 3);
   const Waits wt{g.err, abortf, p.wait_ns};
   int64_t* scan = reinterpret_cast<int64_t*>(smem + p.off_scan);
-  float* ml = reinterpret_cast<float*>(smem + p.off_ml);           // [2 groups][128 rows] {maximum, sum}
+  float2* xml = reinterpret_cast<float2*>(smem + p.off_ml);        // [2 groups][128 rows] {reference maximum, sum}
+  RowsPiece* pieces = reinterpret_cast<RowsPiece*>(smem + p.off_pieces);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool causal = p.tree_mask == nullptr;
   const int toks = TWO ? 2 * p.tile_toks : p.tile_toks;
@@ -263,20 +373,29 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
       mbar_init(&full[i], FP8 ? 4 : 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&empty[i], TWO ? 2 : 1);   // the groups' issuers that read the page
     }
-    for (int i = 0; i < (FP8 ? NRAW : NST); ++i) mbar_init(&raw[i], 1);
-    if constexpr (FP8)
-      for (int i = 0; i < NRAW; ++i) mbar_init(&rawfree[i], 4);
+    for (int i = 0; i < NRAW; ++i) {
+      mbar_init(&raw[i], 1);
+      mbar_init(&rawfree[i], 4);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 1);
-      mbar_init(&pfull[i], 4);
+      mbar_init(&pfull[2 * i], 4);
+      mbar_init(&pfull[2 * i + 1], 4);
       mbar_init(&odone[i], 1);
       mbar_init(&qfull[i], 1);
       mbar_init(&qempty[i], 1);
       mbar_init(&qconv[i], TWO ? 4 : 8);
     }
-    mbar_init(mdone, 1);
+    for (int i = 0; i < kRowsPieces; ++i) {
+      mbar_init(&ifull[i], 1);
+      mbar_init(&iempty[i], 9 + (TWO ? 2 : 1) + (FP8 ? 4 : 0));   // softmax 8, page loads, UMMA issue, conversion 4
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&turn[i], 1);
+      mbar_init(&mdone[i], 1);
+    }
     *abortf = 0;
     fence_mbar_init();
   }
@@ -305,14 +424,20 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
   uint8_t* qbase = smem + p.off_q;
   uint8_t* ring = smem + p.off_ring;
   uint8_t* rring = smem + p.off_raw;
-  const RowsWalk walk{p, scan, toks, causal};
-
-  // second tile present; pages [j0, e) that group s has of a piece [j0, j1)
-  auto has_two = [&](const RowsItem& it) -> bool { return TWO && it.j * toks + p.tile_toks < it.n; };
-  auto group_end = [&](const RowsItem& it, int s, int j0, int j1) -> int {
-    if (!TWO) return j1;
-    if (s == 1 && !has_two(it)) return j0;
-    return min(j1, walk.pages(it, it.j * toks + (s + 1) * p.tile_toks));
+  // The next piece of this CTA, for the whole warp; false at the end, or when
+  // the wait gave up.
+  int piece_at = 0;
+  uint32_t piece_ph = 0;
+  auto next_piece = [&](RowsPiece& it) -> bool {
+    if (!__all_sync(0xffffffffu, mbar_wait(&ifull[piece_at], piece_ph, wt))) return false;
+    it = pieces[piece_at];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&iempty[piece_at]);
+    if (++piece_at == kRowsPieces) {
+      piece_at = 0;
+      piece_ph ^= 1u;
+    }
+    return it.j1 > 0;
   };
 
   if (u0 >= u1) {
@@ -321,7 +446,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
     // ------------------------------------------------------------ page loads
     if (lane == 0) prefetch_tensormap(&kv_map);
     const int64_t vbuf = kGroups;
-    RowsItem it = walk.at(u0);
+    RowsPiece it{};
     int first_b = -1, first_ids = 0;   // pages 0 .. 31 of request first_b, one per lane
     auto ids_of = [&](int b, int j) -> int {
       int s = 0;
@@ -337,10 +462,8 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
     int i = 0;                          // ring index: K page, V page, K page, ...
     int npg = 0;
     bool ok = true, stop = false;
-    for (; it.valid && it.u < u1 && ok && !stop; walk.next(it)) {
-      int j0, j1;
-      walk.piece(it, u0, u1, j0, j1);
-      if (j0 >= j1) continue;
+    while (ok && !stop && next_piece(it)) {
+      const int j0 = it.j0, j1 = it.j1;
       if (first_b != it.b) {
         first_b = it.b;
         first_ids = ids_of(it.b, 0);
@@ -373,11 +496,10 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
             if (lane == 0) {
               if (i >= NST) ok = mbar_wait(&empty[st], static_cast<uint32_t>(i / NST - 1) & 1u, wt);
               if (ok) {
-                uint64_t* bar = kv ? &raw[st] : &full[st];
-                mbar_arrive_expect_tx(bar, TILE);
+                mbar_arrive_expect_tx(&full[st], TILE);
 #pragma unroll
                 for (int hb = 0; hb < HB; ++hb)
-                  tma_load_page(ring + st * TILE + hb * (TILE / HB), &kv_map, bar, hb * 64, it.h,
+                  tma_load_page(ring + st * TILE + hb * (TILE / HB), &kv_map, &full[st], hb * 64, it.h,
                                 static_cast<int>(sub + kv * vbuf));
               }
             }
@@ -386,95 +508,95 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         }
       }
     }
-    // never leave copies in flight.  A stage's V barrier of the bf16 ring
-    // completes once per V page held there, so its parity is counted apart.
+    // never leave copies in flight
     if (lane == 0) {
       const int depth = FP8 ? NRAW : NST;
+      uint64_t* bars = FP8 ? raw : full;
       if (!ok) --i;   // the load that gave up was not issued
-      for (int k = (i > depth ? i - depth : 0); k < i; ++k) {
-        const int st = k % depth;
-        if constexpr (FP8) {
-          mbar_drain(&raw[st], static_cast<uint32_t>(k / depth) & 1u, wt);
-        } else if (k & 1) {
-          mbar_drain(&raw[st], static_cast<uint32_t>(depth % 2 ? k / (2 * depth) : k / depth) & 1u, wt);
-        } else {
-          mbar_drain(&full[st], static_cast<uint32_t>(k / depth) & 1u, wt);
-        }
-      }
+      for (int k = (i > depth ? i - depth : 0); k < i; ++k) mbar_drain(&bars[k % depth], static_cast<uint32_t>(k / depth) & 1u, wt);
     }
     __syncwarp();
   } else if (warp == 11) {
-    // --------------------------------------------------------------- Q loads
-    // TWO: tile s in slot s; else items take the two slots in turn
+    // ------------------------------------------------- schedule and Q loads
+    // Q tiles: TWO: tile s in slot s; else items take the two slots in turn
     if (lane == 0) {
       prefetch_tensormap(&q_map);
+      const RowsWalk walk{p, scan, toks, causal};
       const uint32_t bytes = static_cast<uint32_t>(p.tile_toks * g.group * D * 2);
       int used[2] = {0, 0};
       bool ok = true;
       int seq = 0;
-      for (RowsItem it = walk.at(u0); it.valid && it.u < u1 && ok; walk.next(it)) {
-        int j0, j1;
-        walk.piece(it, u0, u1, j0, j1);
-        if (j0 >= j1) continue;
-        for (int s = 0; s < (TWO ? 2 : 1) && ok; ++s) {
-          if (TWO && group_end(it, s, j0, j1) <= j0) continue;
-          const int slot = TWO ? s : seq & 1;
-          const int k = used[slot]++;
-          if (k > 0) ok = mbar_wait(&qempty[slot], static_cast<uint32_t>(k - 1) & 1u, wt);
-          if (!ok) {
-            --used[slot];
-            break;
+      RowsItem it = walk.at(u0);
+      for (;;) {
+        RowsPiece x{};
+        for (; it.valid && it.u < u1; walk.next(it)) {
+          walk.piece(it, u0, u1, x.j0, x.j1);
+          if (x.j0 < x.j1) break;
+          x.j1 = 0;
+        }
+        if (x.j1 > 0) {
+          x.row0 = it.row0;
+          x.tok0 = it.j * toks;
+          x.n = it.n;
+          x.ctx = it.ctx;
+          x.np = walk.item_pages(it);
+          x.h = it.h;
+          x.b = it.b;
+          x.first = it.u + p.setup;
+          x.e0 = x.e1 = x.j1;
+          if (TWO) {   // the tiles' own ends: the second may be empty, the first see fewer pages
+            x.e0 = min(x.j1, walk.pages(it, x.tok0 + p.tile_toks));
+            x.e1 = x.tok0 + p.tile_toks < x.n ? x.j1 : x.j0;
           }
+        }
+        const int k = seq % kRowsPieces;
+        if (seq >= kRowsPieces) ok = mbar_wait(&iempty[k], static_cast<uint32_t>(seq / kRowsPieces - 1) & 1u, wt);
+        if (!ok) break;
+        pieces[k] = x;
+        mbar_arrive(&ifull[k]);
+        if (x.j1 == 0) break;
+        for (int s = 0; s < (TWO ? 2 : 1) && ok; ++s) {
+          if (TWO && (s ? x.e1 : x.e0) <= x.j0) continue;
+          const int slot = TWO ? s : seq & 1;
+          if (used[slot] > 0) ok = mbar_wait(&qempty[slot], static_cast<uint32_t>(used[slot] - 1) & 1u, wt);
+          if (!ok) break;
+          ++used[slot];
           mbar_arrive_expect_tx(&qfull[slot], bytes);
 #pragma unroll
           for (int hb = 0; hb < HB; ++hb)
-            tma_load_q(qbase + slot * TILE + hb * (TILE / HB), &q_map, &qfull[slot], hb * 64, it.h * g.group,
-                       it.row0 + it.j * toks + s * p.tile_toks);
+            tma_load_q(qbase + slot * TILE + hb * (TILE / HB), &q_map, &qfull[slot], hb * 64, x.h * g.group,
+                       x.row0 + x.tok0 + s * p.tile_toks);
         }
+        if (!ok) break;
         ++seq;
+        walk.next(it);
       }
       for (int s = 0; s < 2; ++s)
         if (used[s] > 0) mbar_drain(&qfull[s], static_cast<uint32_t>(used[s] - 1) & 1u, wt);
     }
     __syncwarp();
-  } else if (warp == 10) {
-    // ---------------------------------------- V relay (bf16): zero rows, hand on
-    if constexpr (!FP8) {
-      int i = 1;
-      uint32_t seen = 0;   // parity bit per stage of `raw`
-      bool ok = true;
-      for (RowsItem it = walk.at(u0); it.valid && it.u < u1 && ok; walk.next(it)) {
-        int j0, j1;
-        walk.piece(it, u0, u1, j0, j1);
-        for (int j = j0; j < j1 && ok; ++j, i += 2) {
-          const int st = i % NST;
-          ok = __all_sync(0xffffffffu, lane != 0 || mbar_wait(&raw[st], (seen >> st) & 1u, wt));
-          if (!ok) break;
-          seen ^= 1u << st;
-          const int live = it.ctx + it.n - j * kPage;   // rows below kv_len
-          if (live < kPage) {
-            mbar_wait(&raw[st], ((seen >> st) & 1u) ^ 1u, wt);   // every lane has seen the copy land
-            for (int c = lane; c < (kPage - live) * 8 * HB; c += 32) {
-              const int hb = c / ((kPage - live) * 8), r = c % ((kPage - live) * 8);
-              *reinterpret_cast<uint4*>(ring + st * TILE + hb * (TILE / HB) + live * 128 + r * 16) = make_uint4(0, 0, 0, 0);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-          }
-          if (lane == 0) mbar_arrive(&full[st]);
-        }
-      }
-    }
-  } else if (warp == 9) {
+  } else if (warp == 9 || (TWO && warp == 10)) {
     // ----------------------------------------------------------- UMMA issue
-    // the whole warp runs the loop, one elected lane issues (umma.cuh)
-    const uint64_t kd0 = umma_desc_sw128(smem_u32(ring)), qd0 = umma_desc_sw128(smem_u32(qbase));
-    const uint64_t vd0 = umma_desc_sw128_mn(smem_u32(ring), TILE / 2);
+    // Steps: PV of a page, then QK of the same group's next page.  The whole
+    // warp runs the loop, one elected lane issues.
+    // TWO: one issuing warp per softmax group, taking strict turns.  One
+    // warp's waits (100-200 cycles each even when nothing is to be waited
+    // for; the tensor core's queue is only a few UMMAs deep) run under the
+    // other's products, and the turns keep the groups half a period apart, so
+    // that one's softmax runs under the other's products too (left alone they
+    // fell into step: 4250 cycles a page).  Both see every use of every ring
+    // stage, pages that only the other tile sees included.
+    // Else one warp for both groups: a stage's uses would alternate between two
+    // issuers, and a parity does not tell a phase from the one two before it.
+    const uint32_t kd0 = static_cast<uint32_t>(umma_desc_sw128(smem_u32(ring)));
+    const uint32_t qd0 = static_cast<uint32_t>(umma_desc_sw128(smem_u32(qbase)));
+    const uint32_t vd0 = static_cast<uint32_t>(umma_desc_sw128_mn(smem_u32(ring), TILE / 2));
+    const uint32_t hi = static_cast<uint32_t>(umma_desc_sw128(0) >> 32);   // the same for all of them
     bool alive = true;
     auto wait1 = [&](uint64_t* bar, uint32_t par) {
-      if (alive) alive = __all_sync(0xffffffffu, lane != 0 || mbar_wait(bar, par, wt));
+      if (alive) alive = __all_sync(0xffffffffu, mbar_wait(bar, par, wt));
     };
-    int kst = 0, vst = 1 % NST;          // ring stages of the next K and V page
+    int kst = 0, vst = 1;                // ring stages of the next K and V page
     uint32_t kph = 0, vph = 0;           // their parities
     auto ring_step = [&](int& st, uint32_t& ph) {
       st += 2;
@@ -483,122 +605,74 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         ph ^= 1u;
       }
     };
-    uint32_t pph[2] = {0, 0};
-    int qn[2] = {0, 0};                  // Q tiles taken from each slot
+    uint32_t pph = 0, qph = 0;           // parities of pfull[s][], of the Q slots (bits)
+    uint32_t tph = warp == 9 ? 1 : 0;    // of turn[s]: group 0 begins
     int seq = 0;
-    auto issue_qk = [&](int s, int slot, int st) {
-      tc_fence_after();
-      const uint64_t qd = desc_add(qd0, static_cast<uint32_t>(slot * TILE)), kd = desc_add(kd0, static_cast<uint32_t>(st * TILE));
-#pragma unroll
-      for (int hb = 0; hb < HB; ++hb) {
-        uint64_t a[4], b[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          a[k] = desc_add(qd, hb * (TILE / HB) + k * 32);
-          b[k] = desc_add(kd, hb * (TILE / HB) + k * 32);
-        }
-        umma4_elect<false>(tmem + static_cast<uint32_t>(s * 128), a, b, IDESC_QK, hb > 0 ? 1u : 0u);
+    RowsPiece it;
+    while (alive && next_piece(it)) {
+      const int j0 = it.j0, s0 = TWO ? warp - 9 : 0, e = s0 == 0 ? it.e0 : it.e1;
+      const int slot = TWO ? s0 : seq & 1, lead = TWO ? 1 : 2;   // QK runs `lead` pages ahead of PV
+      if (j0 < e) {
+        wait1(FP8 ? &qconv[slot] : &qfull[slot], (qph >> slot) & 1u);
+        qph ^= 1u << slot;
       }
-      umma_commit_elect(&sfull[s]);
-    };
-    auto issue_pv = [&](int s, int st, bool first) {
-      wait1(&pfull[s], pph[s]);
-      pph[s] ^= 1u;
-      if (!alive) return;
-      tc_fence_after();
-      const uint64_t vd = desc_add(vd0, static_cast<uint32_t>(st * TILE));
+#pragma unroll 1
+      for (int j = j0 - lead; j < it.j1 && alive; ++j) {
+        const int s = TWO ? s0 : (j - j0) & 1;
+        const uint32_t ts = tmem + static_cast<uint32_t>(s * 128);
+        const bool page = j >= j0, pv = page && j < e, next = j + lead < it.j1, qk = j + lead < e;
+        if (page) {
+          wait1(&full[vst], vph);
+          if constexpr (!FP8) {
+            const int live = it.ctx + it.n - j * kPage;   // V rows past kv_len are zeroed (TWO: by both groups alike)
+            if (live < kPage && alive) {
+              for (int c = lane; c < (kPage - live) * 8; c += 32)
 #pragma unroll
-      for (int h4 = 0; h4 < 2; ++h4) {
-        uint32_t a[4];
-        uint64_t b[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          a[k] = tmem + static_cast<uint32_t>(s * 128 + (4 * h4 + k) * 8);
-          b[k] = desc_add(vd, (4 * h4 + k) * 2048);
-        }
-        umma4_tmem_a_elect<false>(tmem + TM_O + static_cast<uint32_t>(s * 128), a, b, IDESC_PV, (!first || h4 > 0) ? 1u : 0u);
-      }
-    };
-    auto take_q = [&](int slot) {
-      wait1(FP8 ? &qconv[slot] : &qfull[slot], static_cast<uint32_t>(qn[slot]) & 1u);
-      ++qn[slot];
-    };
-    for (RowsItem it = walk.at(u0); it.valid && it.u < u1 && alive; walk.next(it)) {
-      int j0, j1;
-      walk.piece(it, u0, u1, j0, j1);
-      if (j0 >= j1) continue;
-      if constexpr (TWO) {
-        const int e[2] = {group_end(it, 0, j0, j1), group_end(it, 1, j0, j1)};
-        // QK of page j for both tiles, the page's stage freed behind the last
-        auto qk_both = [&](int j, int only) {
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            if ((only >= 0 && s != only) || j >= e[s] || !alive) continue;
-            issue_qk(s, s, kst);
-            if (j == e[s] - 1) umma_commit_elect(&qempty[s]);
+                for (int hb = 0; hb < HB; ++hb)
+                  *reinterpret_cast<uint4*>(ring + vst * TILE + hb * (TILE / HB) + live * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+              fence_proxy_async_smem();
+              __syncwarp();
+            }
           }
-        };
-        for (int s = 0; s < 2; ++s)
-          if (e[s] > j0) take_q(s);
-        wait1(&full[kst], kph);
+        }
+        if (next) wait1(&full[kst], kph);
+        if (pv) wait1(&pfull[2 * s], (pph >> s) & 1u);
+        if constexpr (TWO) {
+          wait1(&turn[s], tph);
+          tph ^= 1u;
+        }
         if (!alive) break;
-        qk_both(j0, -1);
-        umma_commit_elect(&empty[kst]);
-        ring_step(kst, kph);
-        for (int j = j0; j < j1 && alive; ++j) {
-          wait1(&full[vst], vph);
-          bool have_k = false;
-          for (int s = 0; s < 2 && alive; ++s) {
-            if (j < e[s]) {
-              issue_pv(s, vst, j == j0);
-              if (!alive) break;
-              if (j == e[s] - 1) umma_commit_elect(&odone[s]);
-            }
-            if (s == 1) umma_commit_elect(&empty[vst]);
-            if (j + 1 < j1) {
-              if (!have_k) {
-                wait1(&full[kst], kph);
-                have_k = true;
-                if (!alive) break;
-              }
-              qk_both(j + 1, s);
-              if (s == 1) {
-                umma_commit_elect(&empty[kst]);
-                ring_step(kst, kph);
-              }
-            }
-          }
-          ring_step(vst, vph);
+        tc_fence_after();
+        if (pv) {
+          const uint32_t vd = vd0 + static_cast<uint32_t>(vst * (TILE >> 4));
+          umma_pv(ts + TM_O, ts, vd, hi, IDESC_PV, j >= j0 + lead ? 1u : 0u);
+          wait1(&pfull[2 * s + 1], (pph >> s) & 1u);
+          if (!alive) break;
+          tc_fence_after();
+          umma_pv(ts + TM_O, ts + 32, vd + 512, hi, IDESC_PV, 1u);
+          pph ^= 1u << s;
         }
-      } else {
-        const int slot = seq & 1;
-        take_q(slot);
-        auto qk = [&](int j) {
-          wait1(&full[kst], kph);
-          if (!alive) return;
-          issue_qk((j - j0) & 1, slot, kst);
-          umma_commit_elect(&empty[kst]);
-          ring_step(kst, kph);
-          if (j == j1 - 1) umma_commit_elect(&qempty[slot]);
-        };
-        if (alive) qk(j0);
-        if (alive && j0 + 1 < j1) qk(j0 + 1);
-        for (int j = j0; j < j1 && alive; ++j) {
-          const int s = (j - j0) & 1;
-          wait1(&full[vst], vph);
-          if (!alive) break;
-          issue_pv(s, vst, j - j0 < 2);
-          if (!alive) break;
+        if (qk) {
+          umma_qk<HB>(ts, qd0 + static_cast<uint32_t>(slot * (TILE >> 4)), kd0 + static_cast<uint32_t>(kst * (TILE >> 4)), hi,
+                      IDESC_QK);
+          umma_commit_elect(&sfull[s]);
+        }
+        if (TWO && lane == 0) mbar_arrive(&turn[s ^ 1]);
+        if (pv && !qk) umma_commit_elect(&odone[s]);
+        if (page) {
           umma_commit_elect(&empty[vst]);
-          if (j + 2 >= j1) umma_commit_elect(&odone[s]);
           ring_step(vst, vph);
-          if (j + 2 < j1) qk(j + 2);
         }
-        ++seq;
+        if (next) {
+          umma_commit_elect(&empty[kst]);
+          if (j + lead == e - 1) umma_commit_elect(&qempty[slot]);
+          ring_step(kst, kph);
+        }
       }
+      ++seq;
     }
-    umma_commit_elect(mdone);
-    if (lane == 0) mbar_drain(mdone, 0, wt);
+    umma_commit_elect(&mdone[warp - 9]);
+    if (lane == 0) mbar_drain(&mdone[warp - 9], 0, wt);
     __syncwarp();
   } else if (FP8 && warp >= 12) {
     // -------------------------------------------------- E4M3 codes -> f16 tiles
@@ -606,10 +680,9 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
       const int ct = tid - 384, c = ct & 7, r0 = ct >> 3;   // 16-byte chunk of a row, first row
       bool ok = true;
       int i = 0;
-      for (RowsItem it = walk.at(u0); it.valid && it.u < u1 && ok; walk.next(it)) {
-        int j0, j1;
-        walk.piece(it, u0, u1, j0, j1);
-        for (int x = 2 * j0; x < 2 * j1 && ok; ++x, ++i) {
+      RowsPiece it;
+      while (ok && next_piece(it)) {
+        for (int x = 2 * it.j0; x < 2 * it.j1 && ok; ++x, ++i) {
           const int rs = i % NRAW, st = i % NST;
           ok = __all_sync(0xffffffffu, mbar_wait(&raw[rs], static_cast<uint32_t>(i / NRAW) & 1u, wt) &&
                                            (i < NST || mbar_wait(&empty[st], static_cast<uint32_t>(i / NST - 1) & 1u, wt)));
@@ -653,43 +726,41 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         }
       }
     }
-  } else {
+  } else if (warp < 8) {   // (one-tile items leave warp 10 idle)
     // ------------------------------------------------- softmax and epilogue
     const int s = warp >> 2;                        // group
     const int r = tid & 127;                        // row of the tile, TMEM lane
     const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-    const int t = r / g.group, gl = r % g.group;    // token of the tile, head of the group
+    const uint32_t ts = tl + s * 128;               // this row's scores, then its weights
+    const int t = r / g.group;                      // token of the tile
     bool dead = false;
     auto wait_all = [&](uint64_t* bar, uint32_t par) {
       if (!dead) dead = __any_sync(0xffffffffu, !mbar_wait(bar, par, wt));
     };
-    uint32_t sph = 0, oph[2] = {0, 0}, qph = 0;
+    uint32_t sph = 0, oph = 0, qph = 0;             // parities of sfull[s]; odone[], qfull[] (bits)
     int seq = 0;
     bool split = false;                             // this CTA holds the first page of a cut item
-    for (RowsItem it = walk.at(u0); it.valid && it.u < u1; walk.next(it)) {
-      int j0, j1;
-      walk.piece(it, u0, u1, j0, j1);
-      if (j0 >= j1) continue;
-      const int je = group_end(it, s, j0, j1);
-      const int tok = it.j * toks + (TWO ? s * p.tile_toks : 0) + t;   // of the request
+    // The piece stays in shared memory until its end (registers hold scores).
+    for (;; ++seq) {
+      const RowsPiece& it = pieces[seq % kRowsPieces];
+      if (!__all_sync(0xffffffffu, mbar_wait(&ifull[seq % kRowsPieces], static_cast<uint32_t>(seq / kRowsPieces) & 1u, wt)))
+        break;
+      if (it.j1 == 0) break;
+      const int je = s == 0 ? it.e0 : it.e1, ctx = it.ctx;
+      const int tok = it.tok0 + (TWO ? s * p.tile_toks : 0) + t;   // of the request
       const bool live = t < p.tile_toks && tok < it.n;
       float scale = p.scale_log2;
       if constexpr (FP8) {
         // Q row -> f16, scaled by a power of two that brings its largest
-        // magnitude to [2^14, 2^15)
+        // magnitude to [2^14, 2^15).  Where both groups read one tile, both
+        // look at the whole row, then convert a half each.
         const int slot = TWO ? s : seq & 1;
-        const bool have = TWO ? je > j0 : true;
-        if (have) {
-          if (TWO) {
-            wait_all(&qfull[slot], qph);
-            qph ^= 1u;
-          } else {
-            wait_all(&qfull[slot], (qph >> slot) & 1u);
-            qph ^= 1u << slot;
-          }
+        if (!TWO || je > it.j0) {
+          wait_all(&qfull[slot], (qph >> slot) & 1u);
+          qph ^= 1u << slot;
           uint8_t* row = qbase + slot * TILE + r * 128;
           float amax = 0.f;
-#pragma unroll
+#pragma unroll 4
           for (int c = 0; c < 16; ++c) {
             const uint4 v = *reinterpret_cast<const uint4*>(row + (c >> 3) * (TILE / 2) + (((c & 7) ^ (r & 7)) << 4));
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -700,8 +771,8 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
           const float mul = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
           scale *= __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
-          if (!TWO) named_barrier(1, 256);   // both groups have read the rows; each converts one half
-#pragma unroll
+          if (!TWO) named_barrier(1, 256);
+#pragma unroll 4
           for (int c0 = 0; c0 < (TWO ? 16 : 8); ++c0) {
             const int c = TWO ? c0 : s * 8 + c0;
             uint4* q4 = reinterpret_cast<uint4*>(row + (c >> 3) * (TILE / 2) + (((c & 7) ^ (r & 7)) << 4));
@@ -719,136 +790,159 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         }
       }
       const float lazy = kRowsLazy / scale;
-      uint32_t mw[4] = {0, 0, 0, 0};                // tree: this row's mask
-      int bound = live ? it.ctx + tok : -1;         // causal: its last position
-      if (!causal && live) {
-        const uint32_t* m = p.tree_mask + (static_cast<int64_t>(it.row0) + tok) * p.mask_words;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int bits = it.n - 32 * k;           // bits of this word that are nodes
-          if (bits > 0) mw[k] = m[k] & (bits >= 32 ? 0xffffffffu : (1u << bits) - 1u);
-        }
-      }
+      const int bound = live ? ctx + tok : -1;      // causal: its last position
       // first position that some row of the tile does not see
-      const int open = causal ? it.ctx + it.j * toks + (TWO ? s * p.tile_toks : 0) + 1 : it.ctx;
+      const int open = causal ? ctx + it.tok0 + (TWO ? s * p.tile_toks : 0) + 1 : ctx;
       float m = -INFINITY, negm = 0.f, l = 0.f;     // reference maximum (raw), -m scale, sum
-      const int js = TWO ? j0 : j0 + s, step = TWO ? 1 : 2;
-      for (int j = js; j < je; j += step) {
+      for (int j = TWO ? it.j0 : it.j0 + s; j < je; j += TWO ? 1 : 2) {
         wait_all(&sfull[s], sph);
         sph ^= 1u;
         tc_fence_after();
-        uint32_t x[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_async(tl + s * 128 + 32 * c, x[c]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_wait_dep(x[c]);
-        const int pos0 = j * kPage;
-        if (pos0 + kPage > open) {                  // the page holds positions that a row does not see
+        const bool masked = j * kPage + kPage > open;   // the page holds positions that some row does not see
+        uint32_t w[4] = {0, 0, 0, 0};
+        if (masked) {
           if (causal) {
-            const int last = bound - pos0;
-#pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (c > last) x[c >> 5][c & 31] = 0xff800000u;
+            row_window(bound - j * kPage, w);
           } else {
-            uint32_t w[4];
-            tree_window(mw, pos0 - it.ctx, w);
+            uint32_t mw[4];                         // this row's mask: bits below n, none for a dead row
 #pragma unroll
-            for (int c = 0; c < 128; ++c)
-              if (!((w[c >> 5] >> (c & 31)) & 1u)) x[c >> 5][c & 31] = 0xff800000u;
+            for (int k = 0; k < 4; ++k) {
+              const int bits = live ? it.n - 32 * k : 0;
+              mw[k] = bits <= 0 ? 0u
+                                : p.tree_mask[(static_cast<int64_t>(it.row0) + tok) * p.mask_words + k] &
+                                      (bits >= 32 ? 0xffffffffu : (1u << bits) - 1u);
+            }
+            tree_window(mw, j * kPage - ctx, w);
           }
         }
-        float mx[4];
+        // Chunks of 32 columns; the last two are read first and read again for
+        // their exponentials (128 scores in registers spill, and that costs more)
+        uint32_t x[2][32];
+        float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mx[c] = __uint_as_float(x[c][0]);
-#pragma unroll
-          for (int k = 1; k < 31; k += 2) mx[c] = max3(mx[c], __uint_as_float(x[c][k]), __uint_as_float(x[c][k + 1]));
-          mx[c] = fmaxf(mx[c], __uint_as_float(x[c][31]));
+        for (int half = 1; half >= 0; --half) {
+          tmem_ld32_async(ts + 64 * half, x[0]);
+          tmem_ld32_async(ts + 64 * half + 32, x[1]);
+          tmem_ld_wait_dep(x[0]);
+          tmem_ld_wait_dep(x[1]);
+          if (masked) {
+            row_mask(w[2 * half], x[0]);
+            row_mask(w[2 * half + 1], x[1]);
+          }
+          top = max3(top, row_max(x[0]), row_max(x[1]));
         }
-        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-        const bool grow = m != -INFINITY && top > m + lazy;
-        float alpha = 1.f;
-        if (grow || m == -INFINITY) {
-          const float mn = fmaxf(m, top);
-          const float nn = mn == -INFINITY ? 0.f : -mn * scale;
-          if (grow) alpha = fast_exp2(nn - negm);   // 2^((m - mn) scale)
-          m = mn;
+        if (__any_sync(0xffffffffu, top > m + lazy)) {   // (a row without a maximum yet has m = -inf)
+          const bool first = m == -INFINITY;
+          const bool grow = top > m + lazy;
+          if (grow) m = top;
+          const float nn = m == -INFINITY ? 0.f : -m * scale;
+          if (__any_sync(0xffffffffu, grow && !first)) {
+            // S ready: the PV before it has retired, O is stable
+            const float alpha = grow && !first ? fast_exp2(nn - negm) : 1.f;   // 2^((old m - new m) scale)
+            l *= alpha;
+#pragma unroll
+            for (int c0 = 0; c0 < D; c0 += 8) {
+              uint32_t o[8];
+              tmem_ld_async(tl + TM_O + s * 128 + c0, o);
+              tmem_ld_wait_dep(o);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+              tmem_st8(tl + TM_O + s * 128 + c0, o);
+            }
+          }
           negm = nn;
         }
-        if (__any_sync(0xffffffffu, grow)) {
-          // S ready: the PV before it has retired, O is stable
-          l *= alpha;
-#pragma unroll
-          for (int c0 = 0; c0 < D; c0 += 16) {
-            uint32_t w[16];
-            tmem_ld_async(tl + TM_O + s * 128 + c0, w);
-            tmem_ld_wait_dep(w);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(__uint_as_float(w[k]) * alpha);
-            tmem_st16(tl + TM_O + s * 128 + c0, w);
-          }
-        }
-        const float2 sc2 = make_float2(scale, scale), ng2 = make_float2(negm, negm);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[16];
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float2 v = __ffma2_rn(make_float2(__uint_as_float(x[c][2 * k]), __uint_as_float(x[c][2 * k + 1])), sc2, ng2);
-            v.x = fast_exp2(v.x);
-            v.y = fast_exp2(v.y);
-            sum[k & 1] = __fadd2_rn(sum[k & 1], v);
-            w[k] = pack2<FP8>(v.x, v.y);
-          }
-          tmem_st16(tl + s * 128 + 16 * c, w);
+        auto hand_over = [&](int h) {
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&pfull[2 * s + h]);
+        };
+        row_exp<FP8>(ts, 0, x[0], scale, negm, sum[0]);
+        row_exp<FP8>(ts, 1, x[1], scale, negm, sum[1]);
+        tmem_ld32_async(ts + 64, x[0]);
+        tmem_ld32_async(ts + 96, x[1]);
+        hand_over(0);
+        tmem_ld_wait_dep(x[0]);
+        tmem_ld_wait_dep(x[1]);
+        if (masked) {
+          row_mask(w[2], x[0]);
+          row_mask(w[3], x[1]);
         }
+        row_exp<FP8>(ts, 2, x[0], scale, negm, sum[0]);
+        row_exp<FP8>(ts, 3, x[1], scale, negm, sum[1]);
+        hand_over(1);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&pfull[s]);
       }
       // ------------------------------------------------------- end of the piece
-      const int np = walk.item_pages(it);
+      const int j0 = it.j0, j1 = it.j1, np = it.np;
       const bool whole = j0 == 0 && j1 == np;
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (j0 == 0 ? 1 : 0);
       constexpr int ROWS = TWO ? 256 : 128;
       if (j0 == 0 && j1 < np && tid == 0) {
         RowsSplit d;
-        d.b = it.b; d.h = it.h; d.tok0 = it.j * toks; d.n = it.n; d.row0 = it.row0; d.pages = np; d.pad = 0;
-        d.first = it.u + p.setup;
+        d.b = it.b; d.h = it.h; d.tok0 = it.tok0; d.n = it.n; d.row0 = it.row0; d.pages = np; d.pad = 0;
+        d.first = it.first;
         d.W = W;
         d.c_last = static_cast<int>(cta_of_unit(d.first + static_cast<int64_t>(np - 1) * kPage, W, p.num_ctas));
         p.splits[blockIdx.x] = d;
         split = true;
       }
-      const int64_t orow = (static_cast<int64_t>(it.row0 + tok) * g.num_q_heads + static_cast<int64_t>(it.h) * g.group + gl) * D;
-      // D columns (TWO), or this group's half of them, scaled and written
+      // Rows leave through shared memory, SEG bytes of each at a time, so that
+      // a store instruction writes whole sectors (8 segments of 64 bytes, or 16
+      // of 32, instead of 32 of 16): this lane writes 16 bytes of rows
+      // i 32 / CH + lane / CH of its warp.
+      constexpr int SEG = rows_segment(FP8), CH = SEG / 16;
+      uint8_t* stage = smem + p.off_stage + warp * 32 * SEG;
+      int64_t orow[CH];                      // row start in elements (whole: of out, else of this piece's ws_o); -1: dead
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const int rr = 32 * (warp & 3) + i * (32 / CH) + lane / CH, tt = rr / g.group;
+        const int tk = it.tok0 + (TWO ? s * p.tile_toks : 0) + tt;
+        orow[i] = tt >= p.tile_toks || tk >= it.n ? -1
+                  : whole ? (static_cast<int64_t>(it.row0 + tk) * g.num_q_heads + static_cast<int64_t>(it.h) * g.group + rr % g.group) * D
+                          : (slot * ROWS + (TWO ? s * 128 : 0) + rr) * D;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&iempty[seq % kRowsPieces]);
+      const bool f32 = !whole || p.out_f32;
+      uint8_t* obase = whole ? static_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(p.ws_o);
+      const auto swz = [](int row) -> int { return CH == 4 ? (row >> 1) & 3 : (row >> 2) & 1; };
+      // 32 columns of this row from `col` on
       auto store = [&](int col, const float (&v)[32]) {
-        if (!live) return;
-        if (whole && !p.out_f32) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow + col);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            dst[k] = make_uint4(pack2<false>(v[8 * k], v[8 * k + 1]), pack2<false>(v[8 * k + 2], v[8 * k + 3]),
-                                pack2<false>(v[8 * k + 4], v[8 * k + 5]), pack2<false>(v[8 * k + 6], v[8 * k + 7]));
-        } else {
-          float* base = whole ? static_cast<float*>(p.out) + orow
-                              : p.ws_o + (slot * ROWS + (TWO ? s * 128 : 0) + r) * static_cast<int64_t>(D);
-          float4* dst = reinterpret_cast<float4*>(base + col);
+        for (int part = 0; part < 128 / SEG; ++part) {
+          if (!f32 && part >= 64 / SEG) break;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) dst[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          for (int k = 0; k < CH; ++k) {
+            const int u = part * CH + k;     // 16-byte chunk of the 32 columns
+            uint4 w = make_uint4(__float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]), __float_as_uint(v[4 * u + 2]),
+                                 __float_as_uint(v[4 * u + 3]));
+            if (!f32 && u < 4)
+              w = make_uint4(pack2<false>(v[(8 * u) & 31], v[(8 * u + 1) & 31]), pack2<false>(v[(8 * u + 2) & 31], v[(8 * u + 3) & 31]),
+                             pack2<false>(v[(8 * u + 4) & 31], v[(8 * u + 5) & 31]), pack2<false>(v[(8 * u + 6) & 31], v[(8 * u + 7) & 31]));
+            *reinterpret_cast<uint4*>(stage + lane * SEG + ((k ^ swz(lane)) << 4)) = w;
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            const int rr = i * (32 / CH) + lane / CH;
+            const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * SEG + (((lane % CH) ^ swz(rr)) << 4));
+            if (orow[i] >= 0)
+              *reinterpret_cast<uint4*>(obase + (orow[i] + col) * (f32 ? 4 : 2) + part * SEG + 16 * (lane % CH)) = w;
+          }
+          __syncwarp();
         }
       };
       if constexpr (TWO) {
         if (je > j0) {
-          wait_all(&odone[s], oph[s]);
-          oph[s] ^= 1u;
+          wait_all(&odone[s], (oph >> s) & 1u);
+          oph ^= 1u << s;
           tc_fence_after();
         }
         const float f = l == 0.f ? 0.f : (whole ? p.v_scale : 1.f) / l;  // a NaN stays one
-#pragma unroll
+#pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
           uint32_t o[32];
           float v[32];
@@ -862,24 +956,22 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         }
         if (!whole && live) p.ws_lse[slot * ROWS + s * 128 + r] = l == 0.f ? -INFINITY : __log2f(l) - negm;
       } else {
-        // both groups' O of this row lie in this lane: exchange {maximum, sum},
-        // then each group joins and writes half the columns
-        float2* x2 = reinterpret_cast<float2*>(ml);
-        x2[s * 128 + r] = make_float2(l == 0.f ? -INFINITY : -negm, l);
+        // both groups' O of this row lie in this lane: exchange maxima and
+        // sums, then each group joins and writes half the columns
+        xml[s * 128 + r] = make_float2(l == 0.f ? -INFINITY : -negm, l);
         named_barrier(1, 256);
-        const int npieces = min(2, j1 - j0);
-        for (int k = 0; k < npieces; ++k) {
-          wait_all(&odone[k], oph[k]);
-          oph[k] ^= 1u;
+        for (int k = 0; k < min(2, j1 - j0); ++k) {
+          wait_all(&odone[k], (oph >> k) & 1u);
+          oph ^= 1u << k;
         }
         tc_fence_after();
-        const float2 a = x2[r], b = x2[128 + r];
+        const float2 a = xml[r], b = xml[128 + r];
         const float top = fmaxf(a.x, b.x);
         const float wa = a.y == 0.f ? 0.f : fast_exp2(a.x - top), wb = b.y == 0.f ? 0.f : fast_exp2(b.x - top);
         const float lt = wa * a.y + wb * b.y;
         const float f = lt == 0.f ? 0.f : (whole ? p.v_scale : 1.f) / lt;
         const float fa = wa * f, fb = wb * f;   // zero where a group had no weight: its O may be anything
-#pragma unroll
+#pragma unroll 1
         for (int c0 = 0; c0 < D / 2; c0 += 32) {
           uint32_t o[32], q[32];
           float v[32];
@@ -898,7 +990,6 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         named_barrier(1, 256);   // O may be overwritten, the exchange reused
       }
       tc_fence_before();
-      ++seq;
     }
     if (tid == 0 && !split) p.splits[blockIdx.x].b = -1;
   }

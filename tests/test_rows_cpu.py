@@ -39,7 +39,7 @@ def calls(lib, g, rows=80, indptr=16):
     (dict(num_slots=0), INVALID), (dict(kv_dtype=2), INVALID), (dict(sm_scale=0.0), INVALID),
     (dict(sm_scale=float("nan")), INVALID), (dict(k_scale=0.0), INVALID), (dict(v_scale=float("inf")), INVALID),
     (dict(num_ctas=-1), INVALID), (dict(num_ctas=1025), INVALID), (dict(head_dim=96), UNSUPPORTED),
-    (dict(kv_dtype=1, head_dim=64), UNSUPPORTED), (dict(batch=4097), UNSUPPORTED),
+    (dict(kv_dtype=1, head_dim=64), UNSUPPORTED), (dict(batch=2049), UNSUPPORTED),
     (dict(num_q_heads=129, num_kv_heads=1), UNSUPPORTED), (dict(num_slots=1 << 20, slot_stride=8), UNSUPPORTED),
     (dict(max_pages_per_req=(1 << 23) + 1), UNSUPPORTED),
 ])
@@ -47,6 +47,13 @@ def test_geometry(lib, over, status):
     g = geom(**over)
     assert calls(lib, g) == {status}
     assert lib.trtv_workspace_bytes_rows(ctypes.byref(g)) == 0
+
+
+@pytest.mark.parametrize("over", [dict(), dict(head_dim=64), dict(kv_dtype=1)])
+@pytest.mark.parametrize("qo_len", [1, 4096])
+def test_largest_batch(lib, over, qo_len):
+    """Every batch up to the documented limit has a workspace (its shared memory fits)."""
+    assert lib.trtv_workspace_bytes_rows(ctypes.byref(geom(batch=2048, qo_len=qo_len, **over))) > 0
 
 
 def test_null_geometry(lib):

@@ -14,7 +14,10 @@ namespace {
 
 constexpr int kMaxBatch = 2048;   // the requests' scan lies in shared memory
 constexpr int kMaxTreeTokens = 128;
-constexpr int kRowsSetup = 128;  // stream-K charge of an item, in positions
+// stream-K charge of an item in positions: what switching items costs (16384-token
+// prompt 1581 / 1518 / 1467 / 1471 us at 128 / 256 / 384 / 512, packed prompts 639 /
+// 550 / 522 / 532; one-tile items 169 / 171 / 172 us at 128 / 256 / 384)
+constexpr int kRowsSetupTwo = 384, kRowsSetupOne = 128;
 
 // Geometry checks shared by the packed-row calls.
 trtv_status rows_geom(const trtv_geom* g, const int32_t* indptr, int32_t num_tokens, RowsGeom* r) {
@@ -96,9 +99,9 @@ bool rows_smem(const trtv_geom* g, const RowsPlan& pl, RowsAttnParams* p, size_t
   const size_t tile = static_cast<size_t>(kRowsTile) * g->head_dim * 2, raw = static_cast<size_t>(kRowsTile) * g->head_dim;
   const size_t scan = align_up((static_cast<size_t>(g->batch) + 1 + 32) * sizeof(int64_t), 16);
   const size_t ml = pl.two ? 0 : 2 * kRowsTile * 2 * sizeof(float);
-  const size_t bars = (4 * kMaxStages + 32) * sizeof(uint64_t), pieces = 4 * 64;
+  const size_t bars = (4 * kMaxStages + 32) * sizeof(uint64_t), pieces = 4 * 64, rowmap = kRowsTile * 4;
   const size_t stage = static_cast<size_t>(8) * 32 * rows_segment(fp8);
-  const size_t fixed = 2 * tile + ml + stage + pieces + scan + bars + kAlignSlack;
+  const size_t fixed = 2 * tile + ml + stage + rowmap + pieces + scan + bars + kAlignSlack;
   // two stages of codes at least, a third where the requests' scan leaves room
   p->nraw = !fp8 ? 0 : fixed + 3 * raw + 3 * tile <= kSmemOptin ? 3 : 2;
   const size_t codes = p->nraw * raw;
@@ -115,6 +118,8 @@ bool rows_smem(const trtv_geom* g, const RowsPlan& pl, RowsAttnParams* p, size_t
   off += ml;
   p->off_stage = static_cast<int>(off);
   off += stage;
+  p->off_rowmap = static_cast<int>(off);
+  off += rowmap;
   p->off_pieces = static_cast<int>(off);
   off += pieces;
   p->off_scan = static_cast<int>(off);
@@ -182,7 +187,7 @@ trtv_status rows_attn(const trtv_geom* g, const void* q, const void* pool, const
   p.splits = reinterpret_cast<RowsSplit*>(wsb + pl.ws_splits);
   p.out_f32 = out_dtype == TRTV_F32;
   p.num_ctas = pl.num_ctas;
-  p.setup = kRowsSetup;
+  p.setup = pl.two ? kRowsSetupTwo : kRowsSetupOne;
   p.scale_log2 = g->sm_scale * g->k_scale * 1.4426950408889634f;
   p.v_scale = g->v_scale;
   p.wait_ns = wait_limit_ns();

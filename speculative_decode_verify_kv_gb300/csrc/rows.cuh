@@ -111,7 +111,7 @@ struct RowsAttnParams {
   int mask_words, out_f32, num_ctas;
   int tile_toks;               // tokens of a 128-row tile: 128 / group
   int nst, nraw;               // page stages in shared memory; FP8: stages of raw codes
-  int off_q, off_ring, off_raw, off_ml, off_stage, off_pieces, off_scan, off_bar;   // shared memory, from the 1024-aligned base
+  int off_q, off_ring, off_raw, off_ml, off_stage, off_rowmap, off_pieces, off_scan, off_bar;   // shared memory, from the 1024-aligned base
   int setup;                   // what starting an item costs, in positions
   float scale_log2, v_scale;   // sm_scale * k_scale * log2(e)
   uint64_t wait_ns;

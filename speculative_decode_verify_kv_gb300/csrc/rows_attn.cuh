@@ -197,6 +197,15 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// mbar_wait with the waiting loop out of line: a control warp's code runs once
+// per page or item and is fetched each time, so it is kept short.
+static __device__ __noinline__ bool rows_wait_slow(uint64_t* bar, uint32_t parity, int* err, volatile int* abort, uint64_t limit_ns) {
+  return mbar_wait(bar, parity, Waits{err, abort, limit_ns});
+}
+__device__ __forceinline__ bool rows_wait(uint64_t* bar, uint32_t parity, const Waits& w) {
+  return mbar_try_wait(bar, parity) || rows_wait_slow(bar, parity, w.err, w.abort, w.limit_ns);
+}
+
 // K or V page of one head: 128 positions x 64 columns (128 bytes each) per box
 __device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int h, int sub) {
   asm volatile(
@@ -365,6 +374,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
   const Waits wt{g.err, abortf, p.wait_ns};
   int64_t* scan = reinterpret_cast<int64_t*>(smem + p.off_scan);
   float2* xml = reinterpret_cast<float2*>(smem + p.off_ml);        // [2 groups][128 rows] {reference maximum, sum}
+  ushort2* rowmap = reinterpret_cast<ushort2*>(smem + p.off_rowmap);   // [128] {token of the tile, head of the group}
   RowsPiece* pieces = reinterpret_cast<RowsPiece*>(smem + p.off_pieces);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool causal = p.tree_mask == nullptr;
@@ -403,6 +413,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
     tmem_alloc(tslot, 512);
     tmem_relinquish();
   }
+  if (tid < kRowsTile) rowmap[tid] = make_ushort2(static_cast<unsigned short>(tid / g.group), static_cast<unsigned short>(tid % g.group));
   pdl_wait();   // inputs may come from the previous kernel of the stream
   rows_scan(p, toks, causal, scan, scan + g.batch + 1);
   pdl_trigger();
@@ -429,7 +440,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
   int piece_at = 0;
   uint32_t piece_ph = 0;
   auto next_piece = [&](RowsPiece& it) -> bool {
-    if (!__all_sync(0xffffffffu, mbar_wait(&ifull[piece_at], piece_ph, wt))) return false;
+    if (!__all_sync(0xffffffffu, rows_wait(&ifull[piece_at], piece_ph, wt))) return false;
     it = pieces[piece_at];
     __syncwarp();
     if (lane == 0) mbar_arrive(&iempty[piece_at]);
@@ -485,7 +496,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           if constexpr (FP8) {
             const int st = i % NRAW;
             if (lane == 0) {
-              if (i >= NRAW) ok = mbar_wait(&rawfree[st], static_cast<uint32_t>(i / NRAW - 1) & 1u, wt);
+              if (i >= NRAW) ok = rows_wait(&rawfree[st], static_cast<uint32_t>(i / NRAW - 1) & 1u, wt);
               if (ok) {
                 mbar_arrive_expect_tx(&raw[st], RAW);
                 tma_load_page(rring + st * RAW, &kv_map, &raw[st], 0, it.h, static_cast<int>(sub + kv * vbuf));
@@ -494,7 +505,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           } else {
             const int st = i % NST;
             if (lane == 0) {
-              if (i >= NST) ok = mbar_wait(&empty[st], static_cast<uint32_t>(i / NST - 1) & 1u, wt);
+              if (i >= NST) ok = rows_wait(&empty[st], static_cast<uint32_t>(i / NST - 1) & 1u, wt);
               if (ok) {
                 mbar_arrive_expect_tx(&full[st], TILE);
 #pragma unroll
@@ -550,7 +561,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           }
         }
         const int k = seq % kRowsPieces;
-        if (seq >= kRowsPieces) ok = mbar_wait(&iempty[k], static_cast<uint32_t>(seq / kRowsPieces - 1) & 1u, wt);
+        if (seq >= kRowsPieces) ok = rows_wait(&iempty[k], static_cast<uint32_t>(seq / kRowsPieces - 1) & 1u, wt);
         if (!ok) break;
         pieces[k] = x;
         mbar_arrive(&ifull[k]);
@@ -558,7 +569,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         for (int s = 0; s < (TWO ? 2 : 1) && ok; ++s) {
           if (TWO && (s ? x.e1 : x.e0) <= x.j0) continue;
           const int slot = TWO ? s : seq & 1;
-          if (used[slot] > 0) ok = mbar_wait(&qempty[slot], static_cast<uint32_t>(used[slot] - 1) & 1u, wt);
+          if (used[slot] > 0) ok = rows_wait(&qempty[slot], static_cast<uint32_t>(used[slot] - 1) & 1u, wt);
           if (!ok) break;
           ++used[slot];
           mbar_arrive_expect_tx(&qfull[slot], bytes);
@@ -594,7 +605,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
     const uint32_t hi = static_cast<uint32_t>(umma_desc_sw128(0) >> 32);   // the same for all of them
     bool alive = true;
     auto wait1 = [&](uint64_t* bar, uint32_t par) {
-      if (alive) alive = __all_sync(0xffffffffu, mbar_wait(bar, par, wt));
+      if (alive) alive = __all_sync(0xffffffffu, rows_wait(bar, par, wt));
     };
     int kst = 0, vst = 1;                // ring stages of the next K and V page
     uint32_t kph = 0, vph = 0;           // their parities
@@ -635,9 +646,9 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
             }
           }
         }
-        if (next) wait1(&full[kst], kph);
         if (pv) wait1(&pfull[2 * s], (pph >> s) & 1u);
         if constexpr (TWO) {
+          if (next) wait1(&full[kst], kph);
           wait1(&turn[s], tph);
           tph ^= 1u;
         }
@@ -651,6 +662,11 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           tc_fence_after();
           umma_pv(ts + TM_O, ts + 32, vd + 512, hi, IDESC_PV, 1u);
           pph ^= 1u << s;
+        }
+        if (!TWO && qk) {   // (bound by the pages' arrival: not ahead of PV)
+          wait1(&full[kst], kph);
+          if (!alive) break;
+          tc_fence_after();
         }
         if (qk) {
           umma_qk<HB>(ts, qd0 + static_cast<uint32_t>(slot * (TILE >> 4)), kd0 + static_cast<uint32_t>(kst * (TILE >> 4)), hi,
@@ -684,8 +700,8 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
       while (ok && next_piece(it)) {
         for (int x = 2 * it.j0; x < 2 * it.j1 && ok; ++x, ++i) {
           const int rs = i % NRAW, st = i % NST;
-          ok = __all_sync(0xffffffffu, mbar_wait(&raw[rs], static_cast<uint32_t>(i / NRAW) & 1u, wt) &&
-                                           (i < NST || mbar_wait(&empty[st], static_cast<uint32_t>(i / NST - 1) & 1u, wt)));
+          ok = __all_sync(0xffffffffu, rows_wait(&raw[rs], static_cast<uint32_t>(i / NRAW) & 1u, wt) &&
+                                           (i < NST || rows_wait(&empty[st], static_cast<uint32_t>(i / NST - 1) & 1u, wt)));
           if (!ok) break;
           const int live = (x & 1) ? it.ctx + it.n - (x >> 1) * kPage : kPage;   // V rows past kv_len are zeroed
           const uint8_t* src = rring + rs * RAW;
@@ -892,47 +908,71 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
       // Rows leave through shared memory, SEG bytes of each at a time, so that
       // a store instruction writes whole sectors (8 segments of 64 bytes, or 16
       // of 32, instead of 32 of 16): this lane writes 16 bytes of rows
-      // i 32 / CH + lane / CH of its warp.
+      // i 32 / CH + lane / CH of its warp.  (This code runs once per piece: it
+      // is kept short, its instructions come from far away.)
       constexpr int SEG = rows_segment(FP8), CH = SEG / 16;
       uint8_t* stage = smem + p.off_stage + warp * 32 * SEG;
-      int64_t orow[CH];                      // row start in elements (whole: of out, else of this piece's ws_o); -1: dead
+      const bool f32 = !whole || p.out_f32;
+      uint8_t* orow[CH];                     // start of the row (whole: in out, else in this piece's ws_o) + this lane's chunk; null: dead
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-        const int rr = 32 * (warp & 3) + i * (32 / CH) + lane / CH, tt = rr / g.group;
-        const int tk = it.tok0 + (TWO ? s * p.tile_toks : 0) + tt;
-        orow[i] = tt >= p.tile_toks || tk >= it.n ? -1
-                  : whole ? (static_cast<int64_t>(it.row0 + tk) * g.num_q_heads + static_cast<int64_t>(it.h) * g.group + rr % g.group) * D
-                          : (slot * ROWS + (TWO ? s * 128 : 0) + rr) * D;
+        const int rr = 32 * (warp & 3) + i * (32 / CH) + lane / CH;
+        const ushort2 tg = rowmap[rr];
+        const int tk = it.tok0 + (TWO ? s * p.tile_toks : 0) + tg.x;
+        const int64_t row = whole ? static_cast<int64_t>(it.row0 + tk) * g.num_q_heads + it.h * g.group + tg.y
+                                  : slot * ROWS + (TWO ? s * 128 : 0) + rr;
+        orow[i] = tg.x >= p.tile_toks || tk >= it.n
+                      ? nullptr
+                      : (whole ? static_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(p.ws_o)) + row * (D * (f32 ? 4 : 2)) +
+                            16 * (lane % CH);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&iempty[seq % kRowsPieces]);
-      const bool f32 = !whole || p.out_f32;
-      uint8_t* obase = whole ? static_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(p.ws_o);
       const auto swz = [](int row) -> int { return CH == 4 ? (row >> 1) & 3 : (row >> 2) & 1; };
-      // 32 columns of this row from `col` on
-      auto store = [&](int col, const float (&v)[32]) {
+      // this row's next SEG bytes in, the warp's rows' out, `off` bytes into the row
+      auto pass = [&](int off, const uint4 (&w)[CH]) {
 #pragma unroll
-        for (int part = 0; part < 128 / SEG; ++part) {
-          if (!f32 && part >= 64 / SEG) break;
+        for (int k = 0; k < CH; ++k) *reinterpret_cast<uint4*>(stage + lane * SEG + ((k ^ swz(lane)) << 4)) = w[k];
+        __syncwarp();
 #pragma unroll
-          for (int k = 0; k < CH; ++k) {
-            const int u = part * CH + k;     // 16-byte chunk of the 32 columns
-            uint4 w = make_uint4(__float_as_uint(v[4 * u]), __float_as_uint(v[4 * u + 1]), __float_as_uint(v[4 * u + 2]),
-                                 __float_as_uint(v[4 * u + 3]));
-            if (!f32 && u < 4)
-              w = make_uint4(pack2<false>(v[(8 * u) & 31], v[(8 * u + 1) & 31]), pack2<false>(v[(8 * u + 2) & 31], v[(8 * u + 3) & 31]),
-                             pack2<false>(v[(8 * u + 4) & 31], v[(8 * u + 5) & 31]), pack2<false>(v[(8 * u + 6) & 31], v[(8 * u + 7) & 31]));
-            *reinterpret_cast<uint4*>(stage + lane * SEG + ((k ^ swz(lane)) << 4)) = w;
+        for (int i = 0; i < CH; ++i) {
+          const int rr = i * (32 / CH) + lane / CH;
+          const uint4 x = *reinterpret_cast<const uint4*>(stage + rr * SEG + (((lane % CH) ^ swz(rr)) << 4));
+          if (orow[i] != nullptr) *reinterpret_cast<uint4*>(orow[i] + off) = x;
+        }
+        __syncwarp();
+      };
+      // columns [c0, c1) of this row: value(column block of 16, v) gives 16
+      auto store = [&](int c0, int c1, const auto& value) {
+        if (f32) {
+#pragma unroll 1
+          for (int c = c0; c < c1; c += 16) {
+            float v[16];
+            value(c, v);
+#pragma unroll
+            for (int k = 0; k < 4; k += CH) {
+              uint4 w[CH];
+#pragma unroll
+              for (int u = 0; u < CH; ++u)
+                w[u] = make_uint4(__float_as_uint(v[4 * (k + u)]), __float_as_uint(v[4 * (k + u) + 1]),
+                                  __float_as_uint(v[4 * (k + u) + 2]), __float_as_uint(v[4 * (k + u) + 3]));
+              pass(c * 4 + k * 16, w);
+            }
           }
-          __syncwarp();
+        } else {
+#pragma unroll 1
+          for (int c = c0; c < c1; c += 8 * CH) {
+            uint4 w[CH];
 #pragma unroll
-          for (int i = 0; i < CH; ++i) {
-            const int rr = i * (32 / CH) + lane / CH;
-            const uint4 w = *reinterpret_cast<const uint4*>(stage + rr * SEG + (((lane % CH) ^ swz(rr)) << 4));
-            if (orow[i] >= 0)
-              *reinterpret_cast<uint4*>(obase + (orow[i] + col) * (f32 ? 4 : 2) + part * SEG + 16 * (lane % CH)) = w;
+            for (int u = 0; u < CH; u += 2) {
+              float v[16];
+              value(c + 8 * u, v);
+              w[u] = make_uint4(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]), pack2<false>(v[4], v[5]), pack2<false>(v[6], v[7]));
+              w[u + 1] = make_uint4(pack2<false>(v[8], v[9]), pack2<false>(v[10], v[11]), pack2<false>(v[12], v[13]),
+                                    pack2<false>(v[14], v[15]));
+            }
+            pass(c * 2, w);
           }
-          __syncwarp();
         }
       };
       if constexpr (TWO) {
@@ -942,18 +982,14 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           tc_fence_after();
         }
         const float f = l == 0.f ? 0.f : (whole ? p.v_scale : 1.f) / l;  // a NaN stays one
-#pragma unroll 1
-        for (int c0 = 0; c0 < D; c0 += 32) {
-          uint32_t o[32];
-          float v[32];
-          if (je > j0) {
-            tmem_ld32_async(tl + TM_O + s * 128 + c0, o);
-            tmem_ld_wait_dep(o);
-          }
+        const bool none = l == 0.f;   // O may be anything
+        store(0, D, [&](int c, float (&v)[16]) {
+          uint32_t o[16];
+          tmem_ld_async(tl + TM_O + s * 128 + c, o);
+          tmem_ld_wait_dep(o);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = l == 0.f ? 0.f : __uint_as_float(o[k]) * f;
-          store(c0, v);
-        }
+          for (int k = 0; k < 16; ++k) v[k] = none ? 0.f : __uint_as_float(o[k]) * f;
+        });
         if (!whole && live) p.ws_lse[slot * ROWS + s * 128 + r] = l == 0.f ? -INFINITY : __log2f(l) - negm;
       } else {
         // both groups' O of this row lie in this lane: exchange maxima and
@@ -971,20 +1007,16 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         const float lt = wa * a.y + wb * b.y;
         const float f = lt == 0.f ? 0.f : (whole ? p.v_scale : 1.f) / lt;
         const float fa = wa * f, fb = wb * f;   // zero where a group had no weight: its O may be anything
-#pragma unroll 1
-        for (int c0 = 0; c0 < D / 2; c0 += 32) {
-          uint32_t o[32], q[32];
-          float v[32];
-          const int col = s * (D / 2) + c0;
-          tmem_ld32_async(tl + TM_O + col, o);
-          tmem_ld32_async(tl + TM_O + 128 + col, q);
+        store(s * (D / 2), (s + 1) * (D / 2), [&](int c, float (&v)[16]) {
+          uint32_t o[16], q[16];
+          tmem_ld_async(tl + TM_O + c, o);
+          tmem_ld_async(tl + TM_O + 128 + c, q);
           tmem_ld_wait_dep(o);
           tmem_ld_wait_dep(q);
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
+          for (int k = 0; k < 16; ++k)
             v[k] = (fa == 0.f ? 0.f : __uint_as_float(o[k]) * fa) + (fb == 0.f ? 0.f : __uint_as_float(q[k]) * fb);
-          store(col, v);
-        }
+        });
         if (!whole && s == 0 && live) p.ws_lse[slot * ROWS + r] = lt == 0.f ? -INFINITY : top + __log2f(lt);
         tc_fence_before();
         named_barrier(1, 256);   // O may be overwritten, the exchange reused

@@ -33,8 +33,8 @@
 // What bounds a prompt's page is one group's chain: softmax, then PV and the
 // next QK, which cannot start before P is written over S.  So a row's scores are
 // read from TMEM twice (a read of 32 columns takes 35 cycles, spilt registers
-// much more), and P is handed over in two parts, the first three quarters' PV
-// running under the last quarter's exponentials.
+// much more), and P is handed over in two halves, the first half's PV running
+// under the second half's exponentials.
 //
 // Warps: 0-3 and 4-7 softmax groups, 8 page loads, 9 (TWO: and 10) UMMA issue
 // (V rows at or past kv_len are zeroed first: P is zero there but 0 * NaN
@@ -250,8 +250,8 @@ __device__ __forceinline__ void umma_qk(uint32_t d, uint32_t q, uint32_t k, uint
   }
 }
 #undef TRTV_QK_STEP
-//   O (+)= P V: steps of 16 positions, 8 TMEM columns of P and 2 KB of V
-//   apart; the page's first six, or its last two
+//   O (+)= P V for half a page: 4 steps of 16 positions, 8 TMEM columns of P
+//   and 2 KB of V apart
 #define TRTV_PV_STEP(AO, BO, P)                                                          \
   "add.u32 x, %1, " #AO ";\n\tadd.u32 y, %2, " #BO ";\n\tmov.b64 b, {y, %5};\n\t"        \
   "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [x], b, %3, " #P ";\n\t"
@@ -260,17 +260,8 @@ __device__ __forceinline__ void umma_pv(uint32_t d, uint32_t pt, uint32_t v, uin
   asm volatile(
       "{\n\t.reg .pred e, f, t;\n\t.reg .b32 x, y;\n\t.reg .b64 b;\n\telect.sync _|e, 0xffffffff;\n\t"
       "setp.ne.b32 f, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
-      TRTV_PV_STEP(0, 0, f) TRTV_PV_STEP(8, 128, t) TRTV_PV_STEP(16, 256, t)
-      TRTV_PV_STEP(24, 384, t) TRTV_PV_STEP(32, 512, t) TRTV_PV_STEP(40, 640, t)
+      TRTV_PV_STEP(0, 0, f) TRTV_PV_STEP(8, 128, t) TRTV_PV_STEP(16, 256, t) TRTV_PV_STEP(24, 384, t)
       "}\n" ::"r"(d), "r"(pt), "r"(v), "r"(idesc), "r"(accumulate), "r"(desc_hi)
-      : "memory");
-}
-__device__ __forceinline__ void umma_pv_rest(uint32_t d, uint32_t pt, uint32_t v, uint32_t desc_hi, uint32_t idesc) {
-  asm volatile(
-      "{\n\t.reg .pred e, t;\n\t.reg .b32 x, y;\n\t.reg .b64 b;\n\telect.sync _|e, 0xffffffff;\n\t"
-      "setp.eq.b32 t, 0, 0;\n\t"
-      TRTV_PV_STEP(48, 768, t) TRTV_PV_STEP(56, 896, t)
-      "}\n" ::"r"(d), "r"(pt), "r"(v), "r"(idesc), "r"(0), "r"(desc_hi)
       : "memory");
 }
 #undef TRTV_PV_STEP
@@ -369,7 +360,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
   uint64_t* raw = empty + NST;                                     // E4M3: [NRAW] codes landed
   uint64_t* rawfree = raw + NRAW;                                  // E4M3: [NRAW] codes converted
   uint64_t* sfull = rawfree + NRAW;                                // [2] S of group s written
-  uint64_t* pfull = sfull + 2;                                     // [2][2] P of group s: three quarters, the rest, written
+  uint64_t* pfull = sfull + 2;                                     // [2][2] P of group s, half h of the page, written
   uint64_t* odone = pfull + 4;                                     // [2] last PV of the piece retired
   uint64_t* qfull = odone + 2;                                     // [2] Q tile landed
   uint64_t* qempty = qfull + 2;                                    // [2] last QK that reads it retired
@@ -655,13 +646,12 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
             }
           }
         }
-        // (P last: a wait costs 150 cycles even when nothing is to be waited for)
+        if (pv) wait1(&pfull[2 * s], (pph >> s) & 1u);
         if constexpr (TWO) {
           if (next) wait1(&full[kst], kph);
           wait1(&turn[s], tph);
           tph ^= 1u;
         }
-        if (pv) wait1(&pfull[2 * s], (pph >> s) & 1u);
         if (!alive) break;
         tc_fence_after();
         if (pv) {
@@ -670,7 +660,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           wait1(&pfull[2 * s + 1], (pph >> s) & 1u);
           if (!alive) break;
           tc_fence_after();
-          umma_pv_rest(ts + TM_O, ts, vd, hi, IDESC_PV);
+          umma_pv(ts + TM_O, ts + 32, vd + 512, hi, IDESC_PV, 1u);
           pph ^= 1u << s;
         }
         if (!TWO && qk) {   // (bound by the pages' arrival: not ahead of PV)
@@ -841,33 +831,22 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
             tree_window(mw, j * kPage - ctx, w);
           }
         }
-        // Chunks of 32 columns: the last two are read first, and again for their
-        // exponentials (128 scores in registers until then would spill)
-        uint32_t x[2][32], y[2][32];
-        tmem_ld32_async(ts + 64, x[0]);
-        tmem_ld32_async(ts + 96, x[1]);
-        tmem_ld_wait_dep(x[0]);
-        tmem_ld_wait_dep(x[1]);
-        if constexpr (!FP8) {
-          tmem_ld32_async(ts, y[0]);
-          tmem_ld32_async(ts + 32, y[1]);
+        // Chunks of 32 columns; the last two are read first and read again for
+        // their exponentials (128 scores in registers spill, and that costs more)
+        uint32_t x[2][32];
+        float top = -INFINITY;
+#pragma unroll
+        for (int half = 1; half >= 0; --half) {
+          tmem_ld32_async(ts + 64 * half, x[0]);
+          tmem_ld32_async(ts + 64 * half + 32, x[1]);
+          tmem_ld_wait_dep(x[0]);
+          tmem_ld_wait_dep(x[1]);
+          if (masked) {
+            row_mask(w[2 * half], x[0]);
+            row_mask(w[2 * half + 1], x[1]);
+          }
+          top = max3(top, row_max(x[0]), row_max(x[1]));
         }
-        if (masked) {
-          row_mask(w[2], x[0]);
-          row_mask(w[3], x[1]);
-        }
-        float top = fmaxf(row_max(x[0]), row_max(x[1]));
-        if constexpr (FP8) {   // (fewer registers)
-          tmem_ld32_async(ts, y[0]);
-          tmem_ld32_async(ts + 32, y[1]);
-        }
-        tmem_ld_wait_dep(y[0]);
-        tmem_ld_wait_dep(y[1]);
-        if (masked) {
-          row_mask(w[0], y[0]);
-          row_mask(w[1], y[1]);
-        }
-        top = max3(top, row_max(y[0]), row_max(y[1]));
         if (__any_sync(0xffffffffu, top > m + lazy)) {   // (a row without a maximum yet has m = -inf)
           const bool first = m == -INFINITY;
           const bool grow = top > m + lazy;
@@ -896,10 +875,11 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&pfull[2 * s + h]);
         };
-        row_exp<FP8>(ts, 0, y[0], scale, negm, sum[0]);
+        row_exp<FP8>(ts, 0, x[0], scale, negm, sum[0]);
+        row_exp<FP8>(ts, 1, x[1], scale, negm, sum[1]);
         tmem_ld32_async(ts + 64, x[0]);
         tmem_ld32_async(ts + 96, x[1]);
-        row_exp<FP8>(ts, 1, y[1], scale, negm, sum[1]);
+        hand_over(0);
         tmem_ld_wait_dep(x[0]);
         tmem_ld_wait_dep(x[1]);
         if (masked) {
@@ -907,7 +887,6 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           row_mask(w[3], x[1]);
         }
         row_exp<FP8>(ts, 2, x[0], scale, negm, sum[0]);
-        hand_over(0);   // three quarters
         row_exp<FP8>(ts, 3, x[1], scale, negm, sum[1]);
         hand_over(1);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);

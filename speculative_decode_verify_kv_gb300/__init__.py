@@ -300,68 +300,71 @@ def trtv_get_device_error(stream=None) -> int:
 
 
 # -- packed token rows -------------------------------------------------------
-# These calls know their tensors' shapes, so they check them: a buffer that is
-# too small for the geometry would be read out of bounds on the device.
+# These calls know their tensors' shapes, so they check them (a buffer too small
+# for the geometry would be read out of bounds on the device), in few steps: on a
+# small step the host's time is the call's time.
 
-def _arg(fn: str, name: str, x, dtype, shape, none_ok: bool = False, at_least: bool = False) -> int:
-    """Pointer of a contiguous CUDA tensor of `dtype` (one of several) and `shape` (a None entry: any;
-    at_least: or more entries along the first axis)."""
-    if x is None and none_ok:
-        return 0
-    if isinstance(x, int):
+_torch = None
+
+
+def _begin(fn: str, stream):
+    """(current device, raw stream) of a call."""
+    global _torch
+    if _torch is None:
+        import torch
+        torch.cuda.init()
+        _torch = torch
+    dev = _torch.cuda.current_device()
+    if stream is None:
+        return dev, _torch._C._cuda_getCurrentRawStream(dev)
+    return dev, stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _refuse(fn: str, name: str, x, dev: int, dtype, shape):
+    have = f"{x.dtype} {tuple(x.shape)} on {x.device}" if hasattr(x, "dtype") else repr(x)
+    raise ValueError(f"{fn}: {name} is {have}{'' if not hasattr(x, 'is_contiguous') or x.is_contiguous() else ', not contiguous'}; "
+                     f"expected {dtype} {tuple('any' if w is None else w for w in shape)}, contiguous, on the current "
+                     f"device cuda:{dev}")
+
+
+def _arg(fn: str, name: str, x, dev: int, dtype, shape) -> int:
+    """Pointer of a contiguous tensor of this dtype and shape on the current device (a raw pointer passes)."""
+    if x.__class__ is int:
         return x
-    p = _ptr(x)
-    if p and x.get_device() != _device():
-        raise ValueError(f"{fn}: {name} is on cuda:{x.get_device()}, the current device is cuda:{_device()}")
-    if x.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-        raise ValueError(f"{fn}: {name} is {x.dtype}, expected {dtype}")
-    s = tuple(x.shape)
-    if len(s) != len(shape) or any(
-            w is not None and (g < w if at_least and i == 0 else g != w) for i, (g, w) in enumerate(zip(s, shape))):
-        raise ValueError(f"{fn}: {name} has shape {s}, expected {shape}{' or more rows' if at_least else ''}")
-    return p
+    try:
+        if x.dtype is dtype and x.shape == shape and x.get_device() == dev and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(fn, name, x, dev, dtype, shape)
 
 
-def _device() -> int:
-    import torch
-    return torch.cuda.current_device()
-
-
-def _rows_arg(fn: str, name: str, x, rows, heads: int, dim: int):
+def _rows_arg(fn: str, name: str, x, dev: int, shape):
     """Pointer and row pitch of a bf16 [rows, heads, dim] tensor whose rows may lie apart."""
-    import torch
-    if x is None or not x.is_cuda:
-        raise ValueError(f"{fn}: {name} is not a CUDA tensor")
-    if x.get_device() != _device():
-        raise ValueError(f"{fn}: {name} is on cuda:{x.get_device()}, the current device is cuda:{_device()}")
-    if x.dtype != torch.bfloat16 or x.dim() != 3 or tuple(x.shape) != (rows, heads, dim):
-        raise ValueError(f"{fn}: {name} is {x.dtype} {tuple(x.shape)}, expected bf16 {(rows, heads, dim)}")
-    if x.stride(2) != 1 or (heads > 1 and x.stride(1) != dim):
-        raise ValueError(f"{fn}: {name}'s heads of one token are not contiguous")
-    return x.data_ptr(), x.stride(0) if rows > 1 else heads * dim
+    rows, heads, dim = shape
+    if x.dtype is not _torch.bfloat16 or x.shape != shape or x.get_device() != dev:
+        _refuse(fn, name, x, dev, _torch.bfloat16, shape)
+    pitch, head, one = x.stride()
+    if one != 1 or (head != dim and heads > 1):
+        raise ValueError(f"{fn}: {name}'s heads of one token are not contiguous (strides {x.stride()})")
+    return x.data_ptr(), pitch if rows > 1 else heads * dim
 
 
-def _pool_arg(fn: str, geom: Geom, x) -> int:
-    import torch
-    if isinstance(x, int):
+def _pool_arg(fn: str, geom: Geom, x, dev: int) -> int:
+    if x.__class__ is int:
         return x
-    fp8 = geom.kv_dtype == TRTV_FP8_E4M3
-    p = _ptr(x)
-    if x.get_device() != _device():
-        raise ValueError(f"{fn}: kv_pool is on cuda:{x.get_device()}, the current device is cuda:{_device()}")
-    if x.dtype not in ((torch.uint8, torch.float8_e4m3fn) if fp8 else (torch.bfloat16,)):
-        raise ValueError(f"{fn}: kv_pool is {x.dtype}")
     need = geom.num_slots * geom.slot_stride * 128 * geom.num_kv_heads * geom.head_dim
-    if x.numel() < need:
-        raise ValueError(f"{fn}: kv_pool holds {x.numel()} elements, the geometry needs {need}")
-    return p
+    types = (_torch.uint8, _torch.float8_e4m3fn) if geom.kv_dtype == TRTV_FP8_E4M3 else (_torch.bfloat16,)
+    if x.dtype not in types or x.numel() < need or x.get_device() != dev or not x.is_contiguous():
+        _refuse(fn, "kv_pool", x, dev, " or ".join(map(str, types)), (f"{need} elements",))
+    return x.data_ptr()
 
 
-def _tables(fn: str, geom: Geom, page_table, kv_lens, qo_indptr):
-    import torch
-    return (_arg(fn, "page_table", page_table, torch.int32, (geom.batch, geom.max_pages_per_req)),
-            _arg(fn, "kv_lens", kv_lens, torch.int32, (geom.batch,)),
-            _arg(fn, "qo_indptr", qo_indptr, torch.int32, (geom.batch + 1,), none_ok=True))
+def _tables(fn: str, geom: Geom, page_table, kv_lens, qo_indptr, dev: int):
+    i32, b = _torch.int32, geom.batch
+    return (_arg(fn, "page_table", page_table, dev, i32, (b, geom.max_pages_per_req)),
+            _arg(fn, "kv_lens", kv_lens, dev, i32, (b,)),
+            0 if qo_indptr is None else _arg(fn, "qo_indptr", qo_indptr, dev, i32, (b + 1,)))
 
 
 def trtv_norm_rope_stage(geom: Geom, q, k, v, q_weight, k_weight, eps: float, rope_table, rot_dim: int,
@@ -369,74 +372,75 @@ def trtv_norm_rope_stage(geom: Geom, q, k, v, q_weight, k_weight, eps: float, ro
                          stream=None) -> None:
     """Per-head norm of queries and keys, rotation, and K/V staging of packed token rows: q [rows, Hq, D],
     k, v [rows, Hk, D] bf16, each possibly a view of one projection; q_out [rows, Hq, D] bf16."""
-    import torch
     fn = "trtv_norm_rope_stage"
-    rows, D = q.shape[0], geom.head_dim
-    a = NormRope(eps=eps, rot_dim=rot_dim, interleaved=int(interleaved),
-                 table_len=0 if rope_table is None else rope_table.shape[0])
-    a.q, a.q_stride = _rows_arg(fn, "q", q, rows, geom.num_q_heads, D)
-    a.k, a.k_stride = _rows_arg(fn, "k", k, rows, geom.num_kv_heads, D)
-    a.v, a.v_stride = _rows_arg(fn, "v", v, rows, geom.num_kv_heads, D)
-    a.q_weight = _arg(fn, "q_weight", q_weight, torch.bfloat16, (D,), none_ok=True)
-    a.k_weight = _arg(fn, "k_weight", k_weight, torch.bfloat16, (D,), none_ok=True)
-    a.rope_table = _arg(fn, "rope_table", rope_table, torch.float32, (None, rot_dim), none_ok=True)
-    a.positions = _arg(fn, "positions", positions, torch.int32, (rows,), none_ok=True)
-    pt, kl, ip = _tables(fn, geom, page_table, kv_lens, qo_indptr)
-    _check(fn, load().trtv_norm_rope_stage(
-        ctypes.byref(geom), ctypes.byref(a), ip, rows,
-        _arg(fn, "q_out", q_out, torch.bfloat16, (rows, geom.num_q_heads, D)), _pool_arg(fn, geom, kv_pool), pt, kl,
-        _stream(stream)))
+    dev, st = _begin(fn, stream)
+    bf16, d = _torch.bfloat16, geom.head_dim
+    rows = q.shape[0]
+    qs, ks = (rows, geom.num_q_heads, d), (rows, geom.num_kv_heads, d)
+    qp, q_pitch = _rows_arg(fn, "q", q, dev, qs)
+    kp, k_pitch = _rows_arg(fn, "k", k, dev, ks)
+    vp, v_pitch = _rows_arg(fn, "v", v, dev, ks)
+    table_len = 0 if rope_table is None else rope_table.shape[0]
+    a = NormRope(qp, kp, vp, q_pitch, k_pitch, v_pitch,
+                 None if q_weight is None else _arg(fn, "q_weight", q_weight, dev, bf16, (d,)),
+                 None if k_weight is None else _arg(fn, "k_weight", k_weight, dev, bf16, (d,)),
+                 None if rope_table is None else _arg(fn, "rope_table", rope_table, dev, _torch.float32, (table_len, rot_dim)),
+                 None if positions is None else _arg(fn, "positions", positions, dev, _torch.int32, (rows,)),
+                 table_len, rot_dim, 1 if interleaved else 0, eps)
+    pt, kl, ip = _tables(fn, geom, page_table, kv_lens, qo_indptr, dev)
+    _check(fn, load().trtv_norm_rope_stage(ctypes.byref(geom), ctypes.byref(a), ip, rows,
+                                           _arg(fn, "q_out", q_out, dev, bf16, qs), _pool_arg(fn, geom, kv_pool, dev),
+                                           pt, kl, st))
 
 
 def trtv_workspace_bytes_rows(geom: Geom) -> int:
     return load().trtv_workspace_bytes_rows(ctypes.byref(geom))
 
 
-def _ws_arg(fn: str, workspace, ws_bytes: int) -> int:
-    if isinstance(workspace, int):
-        return workspace
-    if workspace.get_device() != _device() or workspace.numel() * workspace.element_size() < ws_bytes:
-        raise ValueError(f"{fn}: workspace on {workspace.device} of {workspace.numel() * workspace.element_size()} bytes, "
-                         f"expected {ws_bytes} on cuda:{_device()}")
-    return _ptr(workspace)
-
-
-def _rows_attn_args(fn: str, geom: Geom, q, kv_pool, page_table, kv_lens, qo_indptr, out, out_dtype: int):
-    import torch
+def _rows_attn(fn: str, geom: Geom, q, kv_pool, page_table, kv_lens, qo_indptr, tree_mask, out, out_dtype: int,
+               workspace, ws_bytes: int, stream) -> None:
+    dev, st = _begin(fn, stream)
     rows = q.shape[0]
     shape = (rows, geom.num_q_heads, geom.head_dim)
-    pt, kl, ip = _tables(fn, geom, page_table, kv_lens, qo_indptr)
-    return (ctypes.byref(geom), _arg(fn, "q", q, torch.bfloat16, shape), _pool_arg(fn, geom, kv_pool), pt, kl, ip, rows,
-            _arg(fn, "out", out, torch.float32 if out_dtype == TRTV_F32 else torch.bfloat16, shape))
+    pt, kl, ip = _tables(fn, geom, page_table, kv_lens, qo_indptr, dev)
+    args = [ctypes.byref(geom), _arg(fn, "q", q, dev, _torch.bfloat16, shape), _pool_arg(fn, geom, kv_pool, dev), pt, kl, ip,
+            rows]
+    if fn == "trtv_verify_tree":
+        uint32 = getattr(_torch, "uint32", None)
+        args.append(_arg(fn, "tree_mask", tree_mask, dev,
+                         uint32 if uint32 is not None and getattr(tree_mask, "dtype", None) is uint32 else _torch.int32,
+                         (rows, (geom.qo_len + 31) // 32)))
+    args.append(_arg(fn, "out", out, dev, _torch.float32 if out_dtype == TRTV_F32 else _torch.bfloat16, shape))
+    if workspace.__class__ is not int:
+        if workspace.get_device() != dev or workspace.nbytes < ws_bytes or not workspace.is_contiguous():
+            _refuse(fn, "workspace", workspace, dev, "any type,", (f"{ws_bytes} bytes",))
+        workspace = workspace.data_ptr()
+    _check(fn, getattr(load(), fn)(*args, out_dtype, workspace, ws_bytes, st))
 
 
 def trtv_prompt_attn(geom: Geom, q, kv_pool, page_table, kv_lens, qo_indptr, out, out_dtype: int, workspace,
                      ws_bytes: int, stream=None) -> None:
     """Causal attention of packed prompts (q, out [rows, Hq, D]) over the paged cache."""
-    *a, o = _rows_attn_args("trtv_prompt_attn", geom, q, kv_pool, page_table, kv_lens, qo_indptr, out, out_dtype)
-    _check("trtv_prompt_attn", load().trtv_prompt_attn(*a, o, out_dtype, _ws_arg("trtv_prompt_attn", workspace, ws_bytes), ws_bytes,
-                                                           _stream(stream)))
+    _rows_attn("trtv_prompt_attn", geom, q, kv_pool, page_table, kv_lens, qo_indptr, None, out, out_dtype, workspace,
+               ws_bytes, stream)
 
 
 def trtv_verify_tree(geom: Geom, q, kv_pool, page_table, kv_lens, qo_indptr, tree_mask, out, out_dtype: int,
                      workspace, ws_bytes: int, stream=None) -> None:
     """Attention of drafted trees over the paged cache; tree_mask int32 [rows, ceil(qo_len / 32)]."""
-    import torch
-    fn = "trtv_verify_tree"
-    *a, o = _rows_attn_args(fn, geom, q, kv_pool, page_table, kv_lens, qo_indptr, out, out_dtype)
-    types = (torch.int32, getattr(torch, "uint32", torch.int32))
-    m = _arg(fn, "tree_mask", tree_mask, types, (q.shape[0], (geom.qo_len + 31) // 32))
-    _check(fn, load().trtv_verify_tree(*a, m, o, out_dtype, _ws_arg(fn, workspace, ws_bytes), ws_bytes, _stream(stream)))
+    _rows_attn("trtv_verify_tree", geom, q, kv_pool, page_table, kv_lens, qo_indptr, tree_mask, out, out_dtype, workspace,
+               ws_bytes, stream)
 
 
 def trtv_tree_commit(geom: Geom, kv_pool, page_table, kv_lens, qo_indptr, path, path_len, new_kv_lens,
                      stream=None) -> None:
     """Accepted path's cache rows to the front of the tree's positions, and the new lengths."""
-    import torch
     fn = "trtv_tree_commit"
-    pt, kl, ip = _tables(fn, geom, page_table, kv_lens, qo_indptr)
-    _check(fn, load().trtv_tree_commit(
-        ctypes.byref(geom), _pool_arg(fn, geom, kv_pool), pt, kl, ip,
-        _arg(fn, "path", path, torch.int32, (geom.batch, None)),
-        _arg(fn, "path_len", path_len, torch.int32, (geom.batch,)), path.shape[1],
-        _arg(fn, "new_kv_lens", new_kv_lens, torch.int32, (geom.batch,)), _stream(stream)))
+    dev, st = _begin(fn, stream)
+    i32, b = _torch.int32, geom.batch
+    pt, kl, ip = _tables(fn, geom, page_table, kv_lens, qo_indptr, dev)
+    width = path.shape[1]
+    _check(fn, load().trtv_tree_commit(ctypes.byref(geom), _pool_arg(fn, geom, kv_pool, dev), pt, kl, ip,
+                                       _arg(fn, "path", path, dev, i32, (b, width)),
+                                       _arg(fn, "path_len", path_len, dev, i32, (b,)), width,
+                                       _arg(fn, "new_kv_lens", new_kv_lens, dev, i32, (b,)), st))

@@ -17,12 +17,15 @@ namespace trtv {
 // D / 8 lanes hold one head: lane l has the 4 + 4 elements that turn together,
 // 4 l .. and rot / 2 + 4 l .. (halves) or 8 l .. and 8 l + 4 .. (interleaved,
 // and the dims past rot), so a rotation needs no other lane and a cosine and a
-// sine load (float4 each) serve every head of the token.  A warp takes
-// heads_per_warp heads of one token (q, then k, then v), kRows rows in flight
-// per lane group.  Bound by the bytes; what a token costs besides (its
-// request, its page, its table row) is loaded once per warp.
-constexpr int kStageThreads = 256;
-constexpr int kStageRows = 4;   // rows in flight per lane group
+// sine load (float4 each) serve every head of the token.  A warp takes a
+// token's heads (q, then k, then v) in batches of kStageRows rows per lane
+// group, the next batch's loads out before this one is worked on; what a token
+// costs besides (its request, its page, its table row) is loaded once.
+// Bound by the bytes: 12 prompts of 13.6 k tokens, 72 heads of 128: 177 us =
+// 6.1 TB/s, 89 % of the copy rate (8 heads a warp and no look-ahead: 294 us;
+// batches of 1 / 3 / 4 rows: 203 / 185 / 195 us; blocks of 256 threads: 189 us).
+constexpr int kStageThreads = 128;
+constexpr int kStageRows = 2;   // rows in flight per lane group, twice
 
 __device__ __forceinline__ void unpack4(uint2 w, float (&x)[4]) {
   x[0] = __uint_as_float(w.x << 16);
@@ -49,41 +52,39 @@ __global__ void __launch_bounds__(kStageThreads) norm_rope_stage_kernel(const __
   constexpr int GPW = 32 / LPR;      // rows a warp holds at a time
   const RowsGeom& g = p.g;
   const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
-  const int heads = g.num_q_heads + 2 * g.num_kv_heads;
-  const int chunks = (heads + p.heads_per_warp - 1) / p.heads_per_warp;
+  const int nq = g.num_q_heads, nqk = nq + g.num_kv_heads, heads = nqk + g.num_kv_heads;
   pdl_wait();
   pdl_trigger();
   if (blockIdx.x == 0) check_spans(g);
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kStageThreads / 32) + (threadIdx.x >> 5);
-  const int64_t tok64 = unit / chunks;
-  if (tok64 >= g.num_tokens) return;
-  const int tok = static_cast<int>(tok64);
-  const int h0 = static_cast<int>(unit % chunks) * p.heads_per_warp, h1 = min(heads, h0 + p.heads_per_warp);
+  if (unit / p.chunks >= g.num_tokens) return;
+  const int tok = static_cast<int>(unit / p.chunks);
+  const int h0 = static_cast<int>(unit % p.chunks) * p.heads_per_warp, h1 = min(heads, h0 + p.heads_per_warp);
   const bool turns = 8 * l < p.rot_dim;
   const bool halves = turns && !p.interleaved;
   const int da = halves ? 4 * l : 8 * l, db = halves ? p.rot_dim / 2 + 4 * l : 8 * l + 4;
 
-  // the first rows' loads go out before the token's request is known
-  auto source = [&](int h) -> const __nv_bfloat16* {
-    if (h < g.num_q_heads) return p.q + tok * p.q_stride + static_cast<int64_t>(h) * D;
-    h -= g.num_q_heads;
-    if (h < g.num_kv_heads) return p.k + tok * p.k_stride + static_cast<int64_t>(h) * D;
-    return p.v + tok * p.v_stride + static_cast<int64_t>(h - g.num_kv_heads) * D;
+  // row h of the token's heads (q, then k, then v): bases such that row h lies h D on
+  const __nv_bfloat16* const qs = p.q + tok * p.q_stride;
+  const __nv_bfloat16* const ks = p.k + tok * p.k_stride - static_cast<int64_t>(nq) * D;
+  const __nv_bfloat16* const vs = p.v + tok * p.v_stride - static_cast<int64_t>(nqk) * D;
+  struct Rows {
+    uint2 a[kStageRows], b[kStageRows];
   };
-  uint2 xa[kStageRows], xb[kStageRows];
-  auto load = [&](int h) {
+  auto load = [&](int h, Rows& x) {
 #pragma unroll
     for (int r = 0; r < kStageRows; ++r) {
       const int hr = h + r * GPW + sub;
-      xa[r] = xb[r] = make_uint2(0, 0);
+      x.a[r] = x.b[r] = make_uint2(0, 0);
       if (hr < h1) {
-        const __nv_bfloat16* s = source(hr);
-        xa[r] = *reinterpret_cast<const uint2*>(s + da);
-        xb[r] = *reinterpret_cast<const uint2*>(s + db);
+        const __nv_bfloat16* s = (hr < nq ? qs : hr < nqk ? ks : vs) + hr * D;
+        x.a[r] = *reinterpret_cast<const uint2*>(s + da);
+        x.b[r] = *reinterpret_cast<const uint2*>(s + db);
       }
     }
   };
-  load(h0);
+  Rows cur;
+  load(h0, cur);   // before the token's request is known
 
   const int b = row_request(g, tok, lane);
   if (b >= g.batch) return;   // equal rows per request, and more of them than requests
@@ -94,8 +95,9 @@ __global__ void __launch_bounds__(kStageThreads) norm_rope_stage_kernel(const __
   const int cell = L - span.n + (tok - span.row0);   // >= 0 and below the capacity when len_ok
   const int pos = p.positions != nullptr ? p.positions[tok] : cell;
   const bool pos_ok = p.rot_dim == 0 || (pos >= 0 && pos < p.table_len);
+  const bool live = len_ok && pos_ok;
   int slot = -1;
-  if (len_ok && pos_ok) {
+  if (live) {
     slot = g.page_table[static_cast<int64_t>(b) * g.max_pages + cell / kPage];
     if (slot < 0 || slot >= g.num_slots) {
       slot = -1;
@@ -105,14 +107,15 @@ __global__ void __launch_bounds__(kStageThreads) norm_rope_stage_kernel(const __
     atomicOr(g.err, len_ok ? TRTV_DEVERR_POSITION : TRTV_DEVERR_KV_LEN);
   }
   float co[4] = {1.f, 1.f, 1.f, 1.f}, si[4] = {0.f, 0.f, 0.f, 0.f};
-  if (turns && len_ok && pos_ok) {
+  if (turns && live) {
     const float* row = p.rope + static_cast<int64_t>(pos) * p.rot_dim + 4 * l;
     const float4 c = *reinterpret_cast<const float4*>(row);
     const float4 s = *reinterpret_cast<const float4*>(row + p.rot_dim / 2);
     co[0] = c.x; co[1] = c.y; co[2] = c.z; co[3] = c.w;
     si[0] = s.x; si[1] = s.y; si[2] = s.z; si[3] = s.w;
   }
-  uint2 wq[2], wk[2];
+  // weights as the heads need them: q's, and from head nq on k's
+  uint2 wq[2] = {}, wk[2] = {};
   if (p.q_weight != nullptr) {
     wq[0] = *reinterpret_cast<const uint2*>(p.q_weight + da);
     wq[1] = *reinterpret_cast<const uint2*>(p.q_weight + db);
@@ -121,17 +124,18 @@ __global__ void __launch_bounds__(kStageThreads) norm_rope_stage_kernel(const __
     wk[0] = *reinterpret_cast<const uint2*>(p.k_weight + da);
     wk[1] = *reinterpret_cast<const uint2*>(p.k_weight + db);
   }
-  const bool live = len_ok && pos_ok;
-  for (int h = h0; h < h1; h += kStageRows * GPW) {
-    if (h > h0) load(h);
+  __nv_bfloat16* const qd = p.q_out + static_cast<int64_t>(tok) * nq * D;
+  const int64_t kd = cell_offset(g, slot < 0 ? 0 : slot, live ? cell : 0, D) - static_cast<int64_t>(nq) * kSub * D;
+  const int64_t vd = kd + static_cast<int64_t>(kGroups - 1) * g.num_kv_heads * kSub * D;   // (one page buffer on, Hk heads later)
+  auto process = [&](int h, const Rows& x) {
 #pragma unroll
     for (int r = 0; r < kStageRows; ++r) {
       const int hr = h + r * GPW + sub;
       if (h + r * GPW >= h1) break;   // the same for the whole warp
-      const bool is_q = hr < g.num_q_heads, is_v = hr >= g.num_q_heads + g.num_kv_heads;
+      const bool is_q = hr < nq, is_v = hr >= nqk;
       float a[4], c[4];
-      unpack4(xa[r], a);
-      unpack4(xb[r], c);
+      unpack4(x.a[r], a);
+      unpack4(x.b[r], c);
       float ss = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) ss += a[i] * a[i] + c[i] * c[i];
@@ -170,13 +174,11 @@ __global__ void __launch_bounds__(kStageThreads) norm_rope_stage_kernel(const __
         }
       }
       if (is_q) {
-        __nv_bfloat16* dst = p.q_out + (static_cast<int64_t>(tok) * g.num_q_heads + hr) * D;
+        __nv_bfloat16* dst = qd + hr * D;
         *reinterpret_cast<uint2*>(dst + da) = live ? pack4(a) : make_uint2(0, 0);
         *reinterpret_cast<uint2*>(dst + db) = live ? pack4(c) : make_uint2(0, 0);
       } else if (slot >= 0) {
-        const int hk = hr - g.num_q_heads - (is_v ? g.num_kv_heads : 0);
-        int64_t off = cell_offset(g, slot, cell, D) + static_cast<int64_t>(hk) * kSub * D;
-        if (is_v) off += static_cast<int64_t>(kGroups) * g.num_kv_heads * kSub * D;
+        const int64_t off = (is_v ? vd : kd) + static_cast<int64_t>(hr) * kSub * D;
         if constexpr (FP8) {
           const float scale = is_v ? p.v_scale : p.k_scale;
           uint8_t* dst = static_cast<uint8_t*>(p.pool) + off;
@@ -184,18 +186,23 @@ __global__ void __launch_bounds__(kStageThreads) norm_rope_stage_kernel(const __
           *reinterpret_cast<uint32_t*>(dst + db) = pack4_e4m3(c, scale);
         } else {
           __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.pool) + off;
-          *reinterpret_cast<uint2*>(dst + da) = is_v ? xa[r] : pack4(a);
-          *reinterpret_cast<uint2*>(dst + db) = is_v ? xb[r] : pack4(c);
+          *reinterpret_cast<uint2*>(dst + da) = is_v ? x.a[r] : pack4(a);
+          *reinterpret_cast<uint2*>(dst + db) = is_v ? x.b[r] : pack4(c);
         }
       }
     }
+  };
+  // the next rows' loads go out before this batch is worked on
+  for (int h = h0; h < h1; h += kStageRows * GPW) {
+    Rows next;
+    if (h + kStageRows * GPW < h1) load(h + kStageRows * GPW, next);
+    process(h, cur);
+    cur = next;
   }
 }
 
 cudaError_t launch_norm_rope_stage(int head_dim, bool fp8, const NormRopeParams& p, cudaStream_t st) {
-  const int heads = p.g.num_q_heads + 2 * p.g.num_kv_heads;
-  const int64_t chunks = (heads + p.heads_per_warp - 1) / p.heads_per_warp;
-  const int64_t warps = chunks * p.g.num_tokens;
+  const int64_t warps = static_cast<int64_t>(p.chunks) * p.g.num_tokens;
   const int64_t blocks = (warps + kStageThreads / 32 - 1) / (kStageThreads / 32);
   const dim3 grid(static_cast<unsigned>(blocks)), block(kStageThreads);
   if (fp8) return launch_pdl(norm_rope_stage_kernel<128, true>, grid, block, 0, st, p);

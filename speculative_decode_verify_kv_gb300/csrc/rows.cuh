@@ -75,7 +75,7 @@ struct NormRopeParams {
   __nv_bfloat16* q_out;
   void* pool;
   int table_len, rot_dim, interleaved;
-  int heads_per_warp;   // heads of a token that one warp takes
+  int heads_per_warp, chunks;   // heads of a token that one warp takes; warps per token
   float eps, k_scale, v_scale;
 };
 

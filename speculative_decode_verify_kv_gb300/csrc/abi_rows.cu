@@ -89,7 +89,7 @@ bool rows_plan(const trtv_geom* g, const RowsGeom& r, RowsPlan* pl) {
   return true;
 }
 
-// Shared memory: Q (two tiles), the page ring, E4M3: the codes' ring, the
+// Shared memory: Q (one or two tiles), the page ring, E4M3: the codes' ring, the
 // groups' exchange, the output rows' staging, the
 // pieces, the requests' scan and its 32 warp totals, barriers.  The ring takes what is left,
 // at most kMaxStages pages.
@@ -101,7 +101,8 @@ bool rows_smem(const trtv_geom* g, const RowsPlan& pl, RowsAttnParams* p, size_t
   const size_t ml = pl.two ? 0 : 2 * kRowsTile * 2 * sizeof(float);
   const size_t bars = (4 * kMaxStages + 32) * sizeof(uint64_t), pieces = 4 * 64, rowmap = kRowsTile * 4;
   const size_t stage = static_cast<size_t>(8) * 32 * rows_segment(fp8);
-  const size_t fixed = 2 * tile + ml + stage + rowmap + pieces + scan + bars + kAlignSlack;
+  const size_t q = (pl.two ? 2 : 1) * tile;
+  const size_t fixed = q + ml + stage + rowmap + pieces + scan + bars + kAlignSlack;
   // two stages of codes at least, a third where the requests' scan leaves room
   p->nraw = !fp8 ? 0 : fixed + 3 * raw + 3 * tile <= kSmemOptin ? 3 : 2;
   const size_t codes = p->nraw * raw;
@@ -109,7 +110,7 @@ bool rows_smem(const trtv_geom* g, const RowsPlan& pl, RowsAttnParams* p, size_t
   p->nst = static_cast<int>(std::min<size_t>((kSmemOptin - fixed - codes) / tile, kMaxStages));
   size_t off = 0;
   p->off_q = 0;
-  off += 2 * tile;
+  off += q;
   p->off_ring = static_cast<int>(off);
   off += p->nst * tile;
   p->off_raw = static_cast<int>(off);

@@ -206,13 +206,24 @@ __device__ __forceinline__ bool rows_wait(uint64_t* bar, uint32_t parity, const 
   return mbar_try_wait(bar, parity) || rows_wait_slow(bar, parity, w.err, w.abort, w.limit_ns);
 }
 
-// K or V page of one head: 128 positions x 64 columns (128 bytes each) per box
-__device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int h, int sub) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(h), "r"(sub), "r"(smem_u32(bar))
-      : "memory");
+// K or V page of one head: 128 positions x 64 columns (128 bytes each) per
+// box.  ONCE: no other item reads the page, it need not stay in L2.
+template <bool ONCE>
+__device__ __forceinline__ void tma_load_page(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int h, int sub,
+                                              uint64_t evict_first) {
+  if constexpr (ONCE) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(h), "r"(sub), "r"(smem_u32(bar)), "l"(evict_first)
+        : "memory");
+  } else {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(0), "r"(h), "r"(sub), "r"(smem_u32(bar))
+        : "memory");
+  }
 }
 
 __device__ __forceinline__ void tma_load_q(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int head, int row) {
@@ -457,6 +468,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
     // ------------------------------------------------------------ page loads
     if (lane == 0) prefetch_tensormap(&kv_map);
     const int64_t vbuf = kGroups;
+    const uint64_t pol = policy_evict_first();
     RowsPiece it{};
     int first_b = -1, first_ids = 0;   // pages 0 .. 31 of request first_b, one per lane
     auto ids_of = [&](int b, int j) -> int {
@@ -499,7 +511,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
               if (i >= NRAW) ok = rows_wait(&rawfree[st], static_cast<uint32_t>(i / NRAW - 1) & 1u, wt);
               if (ok) {
                 mbar_arrive_expect_tx(&raw[st], RAW);
-                tma_load_page(rring + st * RAW, &kv_map, &raw[st], 0, it.h, static_cast<int>(sub + kv * vbuf));
+                tma_load_page<!TWO>(rring + st * RAW, &kv_map, &raw[st], 0, it.h, static_cast<int>(sub + kv * vbuf), pol);
               }
             }
           } else {
@@ -510,8 +522,8 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
                 mbar_arrive_expect_tx(&full[st], TILE);
 #pragma unroll
                 for (int hb = 0; hb < HB; ++hb)
-                  tma_load_page(ring + st * TILE + hb * (TILE / HB), &kv_map, &full[st], hb * 64, it.h,
-                                static_cast<int>(sub + kv * vbuf));
+                  tma_load_page<!TWO>(ring + st * TILE + hb * (TILE / HB), &kv_map, &full[st], hb * 64, it.h,
+                                      static_cast<int>(sub + kv * vbuf), pol);
               }
             }
           }
@@ -529,7 +541,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
     __syncwarp();
   } else if (warp == 11) {
     // ------------------------------------------------- schedule and Q loads
-    // Q tiles: TWO: tile s in slot s; else items take the two slots in turn
+    // Q tiles: TWO: tile s in slot s; else one slot
     if (lane == 0) {
       prefetch_tensormap(&q_map);
       const RowsWalk walk{p, scan, toks, causal};
@@ -568,7 +580,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         if (x.j1 == 0) break;
         for (int s = 0; s < (TWO ? 2 : 1) && ok; ++s) {
           if (TWO && (s ? x.e1 : x.e0) <= x.j0) continue;
-          const int slot = TWO ? s : seq & 1;
+          const int slot = TWO ? s : 0;
           if (used[slot] > 0) ok = rows_wait(&qempty[slot], static_cast<uint32_t>(used[slot] - 1) & 1u, wt);
           if (!ok) break;
           ++used[slot];
@@ -622,7 +634,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
     RowsPiece it;
     while (alive && next_piece(it)) {
       const int j0 = it.j0, s0 = TWO ? warp - 9 : 0, e = s0 == 0 ? it.e0 : it.e1;
-      const int slot = TWO ? s0 : seq & 1, lead = TWO ? 1 : 2;   // QK runs `lead` pages ahead of PV
+      const int slot = TWO ? s0 : 0, lead = TWO ? 1 : 2;   // QK runs `lead` pages ahead of PV
       if (j0 < e) {
         wait1(FP8 ? &qconv[slot] : &qfull[slot], (qph >> slot) & 1u);
         qph ^= 1u << slot;
@@ -770,7 +782,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         // Q row -> f16, scaled by a power of two that brings its largest
         // magnitude to [2^14, 2^15).  Where both groups read one tile, both
         // look at the whole row, then convert a half each.
-        const int slot = TWO ? s : seq & 1;
+        const int slot = TWO ? s : 0;
         if (!TWO || je > it.j0) {
           wait_all(&qfull[slot], (qph >> slot) & 1u);
           qph ^= 1u << slot;

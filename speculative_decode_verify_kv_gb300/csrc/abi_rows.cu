@@ -66,7 +66,7 @@ trtv_status rows_device(RowsGeom* r, const int32_t* page_table, const int32_t* k
 struct RowsPlan {
   bool two;            // 256-row items
   int num_ctas;
-  size_t ws_o, ws_lse, ws_splits, ws_total;
+  size_t ws_o, ws_lse, ws_splits, ws_cont, ws_total;
 };
 
 // 256-row items where a request can fill more than one 128-row tile: its tiles
@@ -85,6 +85,8 @@ bool rows_plan(const trtv_geom* g, const RowsGeom& r, RowsPlan* pl) {
   off = align_up(off + pieces * rows * sizeof(float), 256);
   pl->ws_splits = off;
   off = align_up(off + pl->num_ctas * sizeof(RowsSplit), 256);
+  pl->ws_cont = off;
+  off = align_up(off + pl->num_ctas * sizeof(int), 256);
   pl->ws_total = off;
   return true;
 }
@@ -186,6 +188,7 @@ trtv_status rows_attn(const trtv_geom* g, const void* q, const void* pool, const
   p.ws_o = reinterpret_cast<float*>(wsb + pl.ws_o);
   p.ws_lse = reinterpret_cast<float*>(wsb + pl.ws_lse);
   p.splits = reinterpret_cast<RowsSplit*>(wsb + pl.ws_splits);
+  p.cont = reinterpret_cast<int*>(wsb + pl.ws_cont);
   p.out_f32 = out_dtype == TRTV_F32;
   p.num_ctas = pl.num_ctas;
   p.setup = pl.two ? kRowsSetupTwo : kRowsSetupOne;

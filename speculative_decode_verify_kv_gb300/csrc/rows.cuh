@@ -95,10 +95,9 @@ __host__ __device__ constexpr int rows_segment(bool fp8) { return fp8 ? 32 : 64;
 
 // A row-tile item of the attention that the stream-K split cut: written by the
 // CTA that holds its first page, read by the join kernel.
-struct RowsSplit {
-  int b, h, tok0, n, row0, c_last;  // b < 0: none.  tok0: the item's first token of the request
-  int pages, pad;
-  long long first, W;               // unit of its first page; units of the call
+struct __align__(16) RowsSplit {
+  int b, h, tok0, n;      // b < 0: none.  tok0: the item's first token of the request, n: the request's tokens
+  int row0, c_last, pad0, pad1;   // the request's first row; the CTA of the item's last page
 };
 
 struct RowsAttnParams {
@@ -108,6 +107,7 @@ struct RowsAttnParams {
   float* ws_o;                 // [2 * num_ctas, rows, D] pieces, each normalised by its own sum
   float* ws_lse;               // [2 * num_ctas, rows] log2 of their sums
   RowsSplit* splits;           // [num_ctas]
+  int* cont;                   // [num_ctas] nonzero: the CTA's first piece continues an item that began before it
   int mask_words, out_f32, num_ctas;
   int tile_toks;               // tokens of a 128-row tile: 128 / group
   int nst, nraw;               // page stages in shared memory; FP8: stages of raw codes

@@ -47,6 +47,7 @@
 
 namespace trtv {
 
+constexpr int kRowsLeast = 256;
 constexpr float kRowsLazy = 8.0f;   // log2 of how far a row may outgrow its reference maximum
 
 // ---- items ------------------------------------------------------------------
@@ -87,25 +88,28 @@ struct RowsWalk {
   }
   __device__ __forceinline__ int item_pages(const RowsItem& it) const { return pages(it, (it.j + 1) * toks); }
 
-  // the item that holds unit u (u < scan[batch])
-  __device__ __forceinline__ RowsItem at(int64_t u) const {
-    RowsItem it{};
-    int lo = 0, hi = p.g.batch;          // largest b with scan[b] <= u
+  // the largest i in [0, n) with f(i) <= u, f rising, f(0) <= u: 32 candidates a
+  // round, for the whole warp
+  template <typename F>
+  __device__ __forceinline__ int last_at_most(int n, int64_t u, int lane, F f) const {
+    int lo = 0, hi = n;
     while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (scan[mid] <= u) lo = mid; else hi = mid;
+      const int step = (hi - lo + 31) / 32, i = lo + lane * step;
+      const unsigned m = __ballot_sync(0xffffffffu, i < hi && f(i) <= u);
+      lo += (31 - __clz(m)) * step;
+      hi = min(hi, lo + step);
     }
-    request(it, lo);
-    const int64_t head = (scan[lo + 1] - scan[lo]) / p.g.num_kv_heads;
-    it.h = static_cast<int>((u - scan[lo]) / head);
-    const int64_t base = scan[lo] + it.h * head, r = u - base;
-    int jl = 0, jh = it.nt;              // largest j with before(j) <= r
-    while (jh - jl > 1) {
-      const int mid = (jl + jh) / 2;
-      if (before(it, mid) <= r) jl = mid; else jh = mid;
-    }
-    it.j = jl;
-    it.u = base + before(it, jl);
+    return lo;
+  }
+  // the item that holds unit u (u < scan[batch]), for the whole warp
+  __device__ __forceinline__ RowsItem at(int64_t u, int lane) const {
+    RowsItem it{};
+    request(it, last_at_most(p.g.batch, u, lane, [&](int i) { return scan[i]; }));
+    const int64_t base = scan[it.b], head = before(it, it.nt);
+    it.h = last_at_most(p.g.num_kv_heads, u - base, lane, [&](int i) { return i * head; });
+    it.u = base + it.h * head;
+    it.j = last_at_most(it.nt, u - it.u, lane, [&](int i) { return before(it, i); });
+    it.u += before(it, it.j);
     it.valid = true;
     return it;
   }
@@ -139,6 +143,13 @@ struct __align__(16) RowsPiece {
   int64_t first, pad2;      // unit of its first page
 };
 constexpr int kRowsPieces = 4;   // pieces scheduled ahead
+
+// First unit of CTA c: floor(c W / P), W from the P-th on (c and P are at most
+// 1024, so that little work needs no 64-bit division).
+__device__ __forceinline__ int64_t rows_begin(int64_t c, int64_t W, int64_t P) {
+  if (c >= P) return W;
+  return W < (1 << 22) ? static_cast<uint32_t>(c * W) / static_cast<uint32_t>(P) : cta_unit_begin(c, W, P);
+}
 
 // Units of request b over all its items; 0 when it has none or is left out.
 __device__ __forceinline__ int64_t rows_units(const RowsAttnParams& p, int b, int toks, bool causal, bool flag) {
@@ -429,16 +440,10 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
   rows_scan(p, toks, causal, scan, scan + g.batch + 1);
   pdl_trigger();
   const int64_t W = scan[g.batch];
-  const int64_t u0 = cta_unit_begin(blockIdx.x, W, p.num_ctas), u1 = cta_unit_begin(blockIdx.x + 1, W, p.num_ctas);
-  for (int b = blockIdx.x; b < g.batch; b += gridDim.x) {  // requests with a bad length: zero rows
-    if (scan[b + 1] != scan[b]) continue;
-    const RowSpan s = row_span(g, b);
-    const int64_t o0 = static_cast<int64_t>(s.row0) * g.num_q_heads * D, o1 = o0 + static_cast<int64_t>(s.n) * g.num_q_heads * D;
-    for (int64_t e = o0 + tid; e < o1; e += blockDim.x) {
-      if (p.out_f32) static_cast<float*>(p.out)[e] = 0.f;
-      else static_cast<__nv_bfloat16*>(p.out)[e] = __float2bfloat16(0.f);
-    }
-  }
+  // little work is spread over fewer CTAs: pieces of less than kRowsLeast
+  // positions cost more to join than they save
+  const int64_t P = max(int64_t{1}, min(static_cast<int64_t>(p.num_ctas), W / kRowsLeast));
+  const int64_t u0 = rows_begin(blockIdx.x, W, P), u1 = rows_begin(blockIdx.x + 1, W, P);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -463,7 +468,10 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
   };
 
   if (u0 >= u1) {
-    if (tid == 0) p.splits[blockIdx.x].b = -1;
+    if (tid == 0) {
+      p.splits[blockIdx.x].b = -1;
+      p.cont[blockIdx.x] = 0;
+    }
   } else if (warp == 8) {
     // ------------------------------------------------------------ page loads
     if (lane == 0) prefetch_tensormap(&kv_map);
@@ -542,14 +550,14 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
   } else if (warp == 11) {
     // ------------------------------------------------- schedule and Q loads
     // Q tiles: TWO: tile s in slot s; else one slot
+    const RowsWalk walk{p, scan, toks, causal};
+    RowsItem it = walk.at(u0, lane);
     if (lane == 0) {
       prefetch_tensormap(&q_map);
-      const RowsWalk walk{p, scan, toks, causal};
       const uint32_t bytes = static_cast<uint32_t>(p.tile_toks * g.group * D * 2);
       int used[2] = {0, 0};
       bool ok = true;
       int seq = 0;
-      RowsItem it = walk.at(u0);
       for (;;) {
         RowsPiece x{};
         for (; it.valid && it.u < u1; walk.next(it)) {
@@ -908,12 +916,15 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
       const bool whole = j0 == 0 && j1 == np;
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (j0 == 0 ? 1 : 0);
       constexpr int ROWS = TWO ? 256 : 128;
+      if (seq == 0 && tid == 0) p.cont[blockIdx.x] = j0 > 0;
       if (j0 == 0 && j1 < np && tid == 0) {
-        RowsSplit d;
-        d.b = it.b; d.h = it.h; d.tok0 = it.tok0; d.n = it.n; d.row0 = it.row0; d.pages = np; d.pad = 0;
-        d.first = it.first;
-        d.W = W;
-        d.c_last = static_cast<int>(cta_of_unit(d.first + static_cast<int64_t>(np - 1) * kPage, W, p.num_ctas));
+        RowsSplit d{};
+        d.b = it.b;
+        d.h = it.h;
+        d.tok0 = it.tok0;
+        d.n = it.n;
+        d.row0 = it.row0;
+        d.c_last = static_cast<int>(cta_of_unit(it.first + static_cast<int64_t>(np - 1) * kPage, W, P));
         p.splits[blockIdx.x] = d;
         split = true;
       }
@@ -1036,8 +1047,18 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
       tc_fence_before();
     }
     if (tid == 0 && !split) p.splits[blockIdx.x].b = -1;
+    if (tid == 0 && seq == 0) p.cont[blockIdx.x] = 0;   // no page starts in its units
   }
 
+  for (int b = blockIdx.x; b < g.batch; b += gridDim.x) {  // requests with a bad length: zero rows
+    if (scan[b + 1] != scan[b]) continue;
+    const RowSpan s = row_span(g, b);
+    const int64_t o0 = static_cast<int64_t>(s.row0) * g.num_q_heads * D, o1 = o0 + static_cast<int64_t>(s.n) * g.num_q_heads * D;
+    for (int64_t e = o0 + tid; e < o1; e += blockDim.x) {
+      if (p.out_f32) static_cast<float*>(p.out)[e] = 0.f;
+      else static_cast<__nv_bfloat16*>(p.out)[e] = __float2bfloat16(0.f);
+    }
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 9) {

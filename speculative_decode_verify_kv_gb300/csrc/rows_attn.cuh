@@ -47,6 +47,7 @@
 
 namespace trtv {
 
+constexpr int kConvertWarps = 4;   // warps that convert a tile of E4M3 codes, all of them every tile
 constexpr int kRowsLeast = 256;
 constexpr float kRowsLazy = 8.0f;   // log2 of how far a row may outgrow its reference maximum
 
@@ -201,6 +202,13 @@ __device__ __forceinline__ void rows_scan(const RowsAttnParams& p, int toks, boo
 }
 
 // ---- small device helpers -----------------------------------------------------
+
+// four E4M3 codes -> four f16 (exact)
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -404,12 +412,12 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
 
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
-      mbar_init(&full[i], FP8 ? 4 : 1);
+      mbar_init(&full[i], FP8 ? kConvertWarps : 1);
       mbar_init(&empty[i], TWO ? 2 : 1);   // the groups' issuers that read the page
     }
     for (int i = 0; i < NRAW; ++i) {
       mbar_init(&raw[i], 1);
-      mbar_init(&rawfree[i], 4);
+      mbar_init(&rawfree[i], kConvertWarps);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sfull[i], 1);
@@ -712,45 +720,55 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
     __syncwarp();
   } else if (FP8 && warp >= 12) {
     // -------------------------------------------------- E4M3 codes -> f16 tiles
+    // All four warps work on each tile (a tile each would put two waits per
+    // stage use out of order).  Sixteen threads take rows r and r ^ 5 of an 8-row block:
+    // with the tiles' swizzle (16-byte chunk c of row r at c ^ (r % 8)) every
+    // eight lanes' loads and stores then fall into eight different bank groups.
     if constexpr (FP8) {
-      const int ct = tid - 384, c = ct & 7, r0 = ct >> 3;   // 16-byte chunk of a row, first row
+      constexpr int TT = 32 * kConvertWarps;
+      const int ct = tid - 384;
+      const int c = (ct & 3) + 4 * ((ct >> 3) & 1), odd = (ct >> 2) & 1 ? 5 : 0, g0 = ct >> 4;
+      const int q0 = (c & 3) * 2;
       bool ok = true;
-      int i = 0;
+      int i = 0;              // ring index of the tile
+      int base = 0;           // of the piece's first K page
       RowsPiece it;
       while (ok && next_piece(it)) {
-        for (int x = 2 * it.j0; x < 2 * it.j1 && ok; ++x, ++i) {
+        const int end = base + 2 * (it.j1 - it.j0);
+        for (; i < end && ok; ++i) {
           const int rs = i % NRAW, st = i % NST;
           ok = __all_sync(0xffffffffu, rows_wait(&raw[rs], static_cast<uint32_t>(i / NRAW) & 1u, wt) &&
                                            (i < NST || rows_wait(&empty[st], static_cast<uint32_t>(i / NST - 1) & 1u, wt)));
           if (!ok) break;
-          const int live = (x & 1) ? it.ctx + it.n - (x >> 1) * kPage : kPage;   // V rows past kv_len are zeroed
+          // V rows past kv_len are zeroed
+          const int live = i & 1 ? it.ctx + it.n - (it.j0 + ((i - base) >> 1)) * kPage : kPage;
           const uint8_t* src = rring + rs * RAW;
           uint8_t* dst = ring + st * TILE + (c >> 2) * (TILE / 2);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
+#pragma unroll 2
+          for (int part = 0; part < 8 / kConvertWarps; ++part) {
             uint4 v[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const int r = r0 + 16 * (4 * half + k);
+              const int pair = (4 * part + k) * (TT / 16) + g0, r = ((pair >> 2) << 3) + ((pair & 3) ^ odd);
               v[k] = *reinterpret_cast<const uint4*>(src + r * 128 + ((c ^ (r & 7)) << 4));
+            }
+            if (live < kPage) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int pair = (4 * part + k) * (TT / 16) + g0, r = ((pair >> 2) << 3) + ((pair & 3) ^ odd);
+                if (r >= live) v[k] = make_uint4(0, 0, 0, 0);
+              }
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const int r = r0 + 16 * (4 * half + k);
-              if (r >= live) v[k] = make_uint4(0, 0, 0, 0);
-              const uint32_t in[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-              uint32_t o[8];
-#pragma unroll
-              for (int w = 0; w < 4; ++w) {
-                o[2 * w] = e4m3x2_to_f16x2(static_cast<uint16_t>(in[w] & 0xFFFFu));
-                o[2 * w + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(in[w] >> 16));
-              }
-              // lanes of the two column blocks write opposite chunks first, so
-              // that a row's eight stores fall into eight different banks groups
-              const int f = c >> 2, q0 = (c & 3) * 2;
-              const uint4 a = make_uint4(o[0], o[1], o[2], o[3]), b = make_uint4(o[4], o[5], o[6], o[7]);
-              *reinterpret_cast<uint4*>(dst + r * 128 + (((q0 + f) ^ (r & 7)) << 4)) = f ? b : a;
-              *reinterpret_cast<uint4*>(dst + r * 128 + (((q0 + 1 - f) ^ (r & 7)) << 4)) = f ? a : b;
+              const int pair = (4 * part + k) * (TT / 16) + g0, r = ((pair >> 2) << 3) + ((pair & 3) ^ odd);
+              uint4 a, b;
+              e4m3x4_to_f16x4(v[k].x, a.x, a.y);
+              e4m3x4_to_f16x4(v[k].y, a.z, a.w);
+              e4m3x4_to_f16x4(v[k].z, b.x, b.y);
+              e4m3x4_to_f16x4(v[k].w, b.z, b.w);
+              *reinterpret_cast<uint4*>(dst + r * 128 + ((q0 ^ (r & 7)) << 4)) = a;
+              *reinterpret_cast<uint4*>(dst + r * 128 + (((q0 + 1) ^ (r & 7)) << 4)) = b;
             }
           }
           fence_proxy_async_smem();
@@ -760,6 +778,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
             mbar_arrive(&full[st]);
           }
         }
+        base = end;
       }
     }
   } else if (warp < 8) {   // (one-tile items leave warp 10 idle)

@@ -105,11 +105,19 @@ bool rows_smem(const trtv_geom* g, const RowsPlan& pl, RowsAttnParams* p, size_t
   const size_t stage = static_cast<size_t>(8) * 32 * rows_segment(fp8);
   const size_t q = (pl.two ? 2 : 1) * tile;
   const size_t fixed = q + ml + stage + rowmap + pieces + scan + bars + kAlignSlack;
-  // two stages of codes at least, a third where the requests' scan leaves room
-  p->nraw = !fp8 ? 0 : fixed + 3 * raw + 3 * tile <= kSmemOptin ? 3 : 2;
+  if (fp8) {
+    // four converted tiles and three stages of codes where they fit (one-tile
+    // items: 133 us against 143 with three and five, 64 trees of 16 nodes), else
+    // three; what is left holds codes in flight
+    if (fixed + 2 * raw + 3 * tile > kSmemOptin) return false;
+    p->nst = fixed + 3 * raw + 4 * tile <= kSmemOptin ? 4 : 3;
+    p->nraw = static_cast<int>(std::min<size_t>((kSmemOptin - fixed - p->nst * tile) / raw, kMaxStages));
+  } else {
+    if (fixed + 3 * tile > kSmemOptin) return false;
+    p->nst = static_cast<int>(std::min<size_t>((kSmemOptin - fixed) / tile, kMaxStages));
+    p->nraw = 0;
+  }
   const size_t codes = p->nraw * raw;
-  if (fixed + codes + 3 * tile > kSmemOptin) return false;
-  p->nst = static_cast<int>(std::min<size_t>((kSmemOptin - fixed - codes) / tile, kMaxStages));
   size_t off = 0;
   p->off_q = 0;
   off += q;

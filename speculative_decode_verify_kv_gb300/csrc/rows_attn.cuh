@@ -691,6 +691,11 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           umma_pv(ts + TM_O, ts + 32, vd + 512, hi, IDESC_PV, 1u);
           pph ^= 1u << s;
         }
+        const auto release_v = [&] {
+          umma_commit_elect(&empty[vst]);
+          ring_step(vst, vph);
+        };
+        if (!TWO && page) release_v();   // (with three stages the next K page takes its place)
         if (!TWO && qk) {   // (bound by the pages' arrival: not ahead of PV)
           wait1(&full[kst], kph);
           if (!alive) break;
@@ -703,10 +708,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         }
         if (TWO && lane == 0) mbar_arrive(&turn[s ^ 1]);
         if (pv && !qk) umma_commit_elect(&odone[s]);
-        if (page) {
-          umma_commit_elect(&empty[vst]);
-          ring_step(vst, vph);
-        }
+        if (TWO && page) release_v();
         if (next) {
           umma_commit_elect(&empty[kst]);
           if (j + lead == e - 1) umma_commit_elect(&qempty[slot]);
@@ -725,51 +727,48 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
     // with the tiles' swizzle (16-byte chunk c of row r at c ^ (r % 8)) every
     // eight lanes' loads and stores then fall into eight different bank groups.
     if constexpr (FP8) {
-      constexpr int TT = 32 * kConvertWarps;
+      constexpr int TT = 32 * kConvertWarps, PER = kRowsTile * 8 / TT;   // 16-byte chunks a thread takes of a tile
       const int ct = tid - 384;
       const int c = (ct & 3) + 4 * ((ct >> 3) & 1), odd = (ct >> 2) & 1 ? 5 : 0, g0 = ct >> 4;
       const int q0 = (c & 3) * 2;
+      auto row_of = [&](int k) -> int {
+        const int pair = k * (TT / 16) + g0;
+        return ((pair >> 2) << 3) + ((pair & 3) ^ odd);
+      };
+      int rs = 0, st = 0;              // stages of the codes and of the tile
+      uint32_t rph = 0, sph = 1;       // parities: codes landed, stage free (the first round is)
       bool ok = true;
-      int i = 0;              // ring index of the tile
-      int base = 0;           // of the piece's first K page
       RowsPiece it;
       while (ok && next_piece(it)) {
-        const int end = base + 2 * (it.j1 - it.j0);
-        for (; i < end && ok; ++i) {
-          const int rs = i % NRAW, st = i % NST;
-          ok = __all_sync(0xffffffffu, rows_wait(&raw[rs], static_cast<uint32_t>(i / NRAW) & 1u, wt) &&
-                                           (i < NST || rows_wait(&empty[st], static_cast<uint32_t>(i / NST - 1) & 1u, wt)));
+        for (int x = 2 * it.j0; x < 2 * it.j1; ++x) {
+          ok = __all_sync(0xffffffffu, rows_wait(&raw[rs], rph, wt));
           if (!ok) break;
-          // V rows past kv_len are zeroed
-          const int live = i & 1 ? it.ctx + it.n - (it.j0 + ((i - base) >> 1)) * kPage : kPage;
           const uint8_t* src = rring + rs * RAW;
           uint8_t* dst = ring + st * TILE + (c >> 2) * (TILE / 2);
-#pragma unroll 2
-          for (int part = 0; part < 8 / kConvertWarps; ++part) {
-            uint4 v[4];
+          uint4 v[PER];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int pair = (4 * part + k) * (TT / 16) + g0, r = ((pair >> 2) << 3) + ((pair & 3) ^ odd);
-              v[k] = *reinterpret_cast<const uint4*>(src + r * 128 + ((c ^ (r & 7)) << 4));
-            }
-            if (live < kPage) {
+          for (int k = 0; k < PER; ++k) {
+            const int r = row_of(k);
+            v[k] = *reinterpret_cast<const uint4*>(src + r * 128 + ((c ^ (r & 7)) << 4));
+          }
+          const int live = x & 1 ? it.ctx + it.n - (x >> 1) * kPage : kPage;   // V rows past kv_len are zeroed
+          if (live < kPage) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int pair = (4 * part + k) * (TT / 16) + g0, r = ((pair >> 2) << 3) + ((pair & 3) ^ odd);
-                if (r >= live) v[k] = make_uint4(0, 0, 0, 0);
-              }
-            }
+            for (int k = 0; k < PER; ++k)
+              if (row_of(k) >= live) v[k] = make_uint4(0, 0, 0, 0);
+          }
+          ok = __all_sync(0xffffffffu, rows_wait(&empty[st], sph, wt));
+          if (!ok) break;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const int pair = (4 * part + k) * (TT / 16) + g0, r = ((pair >> 2) << 3) + ((pair & 3) ^ odd);
-              uint4 a, b;
-              e4m3x4_to_f16x4(v[k].x, a.x, a.y);
-              e4m3x4_to_f16x4(v[k].y, a.z, a.w);
-              e4m3x4_to_f16x4(v[k].z, b.x, b.y);
-              e4m3x4_to_f16x4(v[k].w, b.z, b.w);
-              *reinterpret_cast<uint4*>(dst + r * 128 + ((q0 ^ (r & 7)) << 4)) = a;
-              *reinterpret_cast<uint4*>(dst + r * 128 + (((q0 + 1) ^ (r & 7)) << 4)) = b;
-            }
+          for (int k = 0; k < PER; ++k) {
+            const int r = row_of(k);
+            uint4 a, b;
+            e4m3x4_to_f16x4(v[k].x, a.x, a.y);
+            e4m3x4_to_f16x4(v[k].y, a.z, a.w);
+            e4m3x4_to_f16x4(v[k].z, b.x, b.y);
+            e4m3x4_to_f16x4(v[k].w, b.z, b.w);
+            *reinterpret_cast<uint4*>(dst + r * 128 + ((q0 ^ (r & 7)) << 4)) = a;
+            *reinterpret_cast<uint4*>(dst + r * 128 + (((q0 + 1) ^ (r & 7)) << 4)) = b;
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -777,8 +776,15 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
             mbar_arrive(&rawfree[rs]);
             mbar_arrive(&full[st]);
           }
+          if (++rs == NRAW) {
+            rs = 0;
+            rph ^= 1u;
+          }
+          if (++st == NST) {
+            st = 0;
+            sph ^= 1u;
+          }
         }
-        base = end;
       }
     }
   } else if (warp < 8) {   // (one-tile items leave warp 10 idle)

@@ -203,6 +203,17 @@ __device__ __forceinline__ void rows_scan(const RowsAttnParams& p, int toks, boo
 
 // ---- small device helpers -----------------------------------------------------
 
+// Named barrier; whether every thread brought true.
+__device__ __forceinline__ bool barrier_all(int id, int threads, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbar.red.and.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(x))
+      : "memory");
+  return r != 0;
+}
+
 // four E4M3 codes -> four f16 (exact)
 __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
   asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
@@ -804,8 +815,11 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
     // The piece stays in shared memory until its end (registers hold scores).
     for (;; ++seq) {
       const RowsPiece& it = pieces[seq % kRowsPieces];
-      if (!__all_sync(0xffffffffu, mbar_wait(&ifull[seq % kRowsPieces], static_cast<uint32_t>(seq / kRowsPieces) & 1u, wt)))
-        break;
+      bool got = mbar_wait(&ifull[seq % kRowsPieces], static_cast<uint32_t>(seq / kRowsPieces) & 1u, wt);
+      // one-tile items meet at barriers below: all go on, or (a wait of the CTA
+      // gave up meanwhile) none
+      got = TWO ? __all_sync(0xffffffffu, got) : barrier_all(1, 256, got);
+      if (!got) break;
       if (it.j1 == 0) break;
       const int je = s == 0 ? it.e0 : it.e1, ctx = it.ctx;
       const int tok = it.tok0 + (TWO ? s * p.tile_toks : 0) + t;   // of the request
@@ -990,13 +1004,17 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         }
         __syncwarp();
       };
-      // columns [c0, c1) of this row: value(column block of 16, v) gives 16
-      auto store = [&](int c0, int c1, const auto& value) {
+      // columns [c0, c1) of this row: fetch(c, u) starts reading 16 columns into
+      // buffer u, take(c, u, v) gives them; the next block's read runs under a
+      // pass (E4M3: read when taken, its registers are fewer: 151 against 160 us)
+      auto store = [&](int c0, int c1, const auto& fetch, const auto& take) {
         if (f32) {
+          fetch(c0, 0);
 #pragma unroll 1
           for (int c = c0; c < c1; c += 16) {
             float v[16];
-            value(c, v);
+            take(c, 0, v);
+            if (c + 16 < c1) fetch(c + 16, 0);
 #pragma unroll
             for (int k = 0; k < 4; k += CH) {
               uint4 w[CH];
@@ -1008,21 +1026,28 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
             }
           }
         } else {
+#pragma unroll
+          for (int u = 0; u < CH / 2; ++u) fetch(c0 + 16 * u, u);
 #pragma unroll 1
           for (int c = c0; c < c1; c += 8 * CH) {
             uint4 w[CH];
 #pragma unroll
-            for (int u = 0; u < CH; u += 2) {
+            for (int u = 0; u < CH / 2; ++u) {
               float v[16];
-              value(c + 8 * u, v);
-              w[u] = make_uint4(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]), pack2<false>(v[4], v[5]), pack2<false>(v[6], v[7]));
-              w[u + 1] = make_uint4(pack2<false>(v[8], v[9]), pack2<false>(v[10], v[11]), pack2<false>(v[12], v[13]),
-                                    pack2<false>(v[14], v[15]));
+              take(c + 16 * u, u, v);
+              w[2 * u] = make_uint4(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]), pack2<false>(v[4], v[5]), pack2<false>(v[6], v[7]));
+              w[2 * u + 1] = make_uint4(pack2<false>(v[8], v[9]), pack2<false>(v[10], v[11]), pack2<false>(v[12], v[13]),
+                                        pack2<false>(v[14], v[15]));
+            }
+            if (c + 8 * CH < c1) {
+#pragma unroll
+              for (int u = 0; u < CH / 2; ++u) fetch(c + 8 * CH + 16 * u, u);
             }
             pass(c * 2, w);
           }
         }
       };
+      uint32_t o[2][16];
       if constexpr (TWO) {
         if (je > j0) {
           wait_all(&odone[s], (oph >> s) & 1u);
@@ -1031,13 +1056,17 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         }
         const float f = l == 0.f ? 0.f : (whole ? p.v_scale : 1.f) / l;  // a NaN stays one
         const bool none = l == 0.f;   // O may be anything
-        store(0, D, [&](int c, float (&v)[16]) {
-          uint32_t o[16];
-          tmem_ld_async(tl + TM_O + s * 128 + c, o);
-          tmem_ld_wait_dep(o);
+        store(
+            0, D,
+            [&](int c, int u) {
+              if constexpr (!FP8) tmem_ld_async(tl + TM_O + s * 128 + c, o[u]);
+            },
+            [&](int c, int u, float (&v)[16]) {
+              if constexpr (FP8) tmem_ld_async(tl + TM_O + s * 128 + c, o[u]);
+              tmem_ld_wait_dep(o[u]);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) v[k] = none ? 0.f : __uint_as_float(o[k]) * f;
-        });
+              for (int k = 0; k < 16; ++k) v[k] = none ? 0.f : __uint_as_float(o[u][k]) * f;
+            });
         if (!whole && live) p.ws_lse[slot * ROWS + s * 128 + r] = l == 0.f ? -INFINITY : __log2f(l) - negm;
       } else {
         // both groups' O of this row lie in this lane: exchange maxima and
@@ -1055,16 +1084,26 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         const float lt = wa * a.y + wb * b.y;
         const float f = lt == 0.f ? 0.f : (whole ? p.v_scale : 1.f) / lt;
         const float fa = wa * f, fb = wb * f;   // zero where a group had no weight: its O may be anything
-        store(s * (D / 2), (s + 1) * (D / 2), [&](int c, float (&v)[16]) {
-          uint32_t o[16], q[16];
-          tmem_ld_async(tl + TM_O + c, o);
-          tmem_ld_async(tl + TM_O + 128 + c, q);
-          tmem_ld_wait_dep(o);
-          tmem_ld_wait_dep(q);
+        uint32_t q[2][16];
+        store(
+            s * (D / 2), (s + 1) * (D / 2),
+            [&](int c, int u) {
+              if constexpr (!FP8) {
+                tmem_ld_async(tl + TM_O + c, o[u]);
+                tmem_ld_async(tl + TM_O + 128 + c, q[u]);
+              }
+            },
+            [&](int c, int u, float (&v)[16]) {
+              if constexpr (FP8) {
+                tmem_ld_async(tl + TM_O + c, o[u]);
+                tmem_ld_async(tl + TM_O + 128 + c, q[u]);
+              }
+              tmem_ld_wait_dep(o[u]);
+              tmem_ld_wait_dep(q[u]);
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            v[k] = (fa == 0.f ? 0.f : __uint_as_float(o[k]) * fa) + (fb == 0.f ? 0.f : __uint_as_float(q[k]) * fb);
-        });
+              for (int k = 0; k < 16; ++k)
+                v[k] = (fa == 0.f ? 0.f : __uint_as_float(o[u][k]) * fa) + (fb == 0.f ? 0.f : __uint_as_float(q[u][k]) * fb);
+            });
         if (!whole && s == 0 && live) p.ws_lse[slot * ROWS + r] = lt == 0.f ? -INFINITY : top + __log2f(lt);
         tc_fence_before();
         named_barrier(1, 256);   // O may be overwritten, the exchange reused

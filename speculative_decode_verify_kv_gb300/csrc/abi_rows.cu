@@ -187,6 +187,8 @@ trtv_status rows_attn(const trtv_geom* g, const void* q, const void* pool, const
   if (!rows_smem(g, pl, &p, &smem)) return TRTV_ERR_UNSUPPORTED;
   if ((s = rows_device(&p.g, page_table, kv_lens)) != TRTV_OK) return s;
   p.tile_toks = kRowsTile / p.g.group;
+  p.items = mask != nullptr && pl.two ? (g->qo_len + 2 * p.tile_toks - 1) / (2 * p.tile_toks) : 1;
+  if (p.items > pl.num_ctas) p.items = 1;
   CUtensorMap kv_map, q_map;
   if (!encode_pages(g, pool, &kv_map) || !encode_rows(g, p.g, p.tile_toks, q, &q_map)) return TRTV_ERR_CUDA;
   uint8_t* wsb = static_cast<uint8_t*>(ws);

@@ -97,7 +97,7 @@ __host__ __device__ constexpr int rows_segment(bool fp8) { return fp8 ? 32 : 64;
 // CTA that holds its first page, read by the join kernel.
 struct __align__(16) RowsSplit {
   int b, h, tok0, n;      // b < 0: none.  tok0: the item's first token of the request, n: the request's tokens
-  int row0, c_last, pad0, pad1;   // the request's first row; the CTA of the item's last page
+  int row0, c_last, stride, pad;  // the request's first row; the CTA of the item's last page; from one of its CTAs to the next
 };
 
 struct RowsAttnParams {
@@ -110,6 +110,7 @@ struct RowsAttnParams {
   int* cont;                   // [num_ctas] nonzero: the CTA's first piece continues an item that began before it
   int mask_words, out_f32, num_ctas;
   int tile_toks;               // tokens of a 128-row tile: 128 / group
+  int items;                   // trees: 256-row items that the largest has per KV head; else 1
   int nst, nraw;               // page stages in shared memory; FP8: stages of raw codes
   int off_q, off_ring, off_raw, off_ml, off_stage, off_rowmap, off_pieces, off_scan, off_bar;   // shared memory, from the 1024-aligned base
   int setup;                   // what starting an item costs, in positions

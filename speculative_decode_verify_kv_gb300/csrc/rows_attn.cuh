@@ -14,7 +14,9 @@
 // units of cache positions: a prompt tile's cost is then a quadratic in its
 // index, with no rounding to sum, and a page belongs to the CTA that holds its
 // first position).  Pieces of an item cut between CTAs are joined by
-// rows_join_kernel.
+// rows_join_kernel.  LANES: a tree of more than 256 rows has several items a KV
+// head that read the same pages; the CTAs walk in as many lanes, abreast (see
+// rows_scan; 16 trees of 512 rows over 16-32 k positions: 320 -> 301 us).
 //
 // Per page and tile: S = Q K^T (128 x 128, fp32 in TMEM), softmax in registers
 // (running maximum, moved only when it rises by more than 2^8; sums in fp32 of
@@ -60,11 +62,13 @@ struct RowsItem {
   bool valid;
 };
 
+template <bool LANES>
 struct RowsWalk {
   const RowsAttnParams& p;
   const int64_t* scan;   // [batch + 1] units before each request
   int toks;              // tokens per item
   bool causal;
+  int lane_item;         // >= 0: this CTA takes item `lane_item` of every KV head, scan counts one item a head
 
   __device__ __forceinline__ int64_t cost(const RowsItem& it) const {
     return p.setup + (causal ? static_cast<int64_t>(it.ctx) + static_cast<int64_t>(toks) * (it.j + 1)
@@ -106,18 +110,24 @@ struct RowsWalk {
   __device__ __forceinline__ RowsItem at(int64_t u, int lane) const {
     RowsItem it{};
     request(it, last_at_most(p.g.batch, u, lane, [&](int i) { return scan[i]; }));
-    const int64_t base = scan[it.b], head = before(it, it.nt);
+    const int64_t base = scan[it.b], head = before(it, LANES && lane_item >= 0 ? 1 : it.nt);
     it.h = last_at_most(p.g.num_kv_heads, u - base, lane, [&](int i) { return i * head; });
     it.u = base + it.h * head;
-    it.j = last_at_most(it.nt, u - it.u, lane, [&](int i) { return before(it, i); });
-    it.u += before(it, it.j);
+    if (LANES && lane_item >= 0) {
+      it.j = lane_item;
+    } else {
+      it.j = last_at_most(it.nt, u - it.u, lane, [&](int i) { return before(it, i); });
+      it.u += before(it, it.j);
+    }
     it.valid = true;
     return it;
   }
   __device__ __forceinline__ void next(RowsItem& it) const {
     it.u += cost(it);
-    if (++it.j < it.nt) return;
-    it.j = 0;
+    if (!LANES || lane_item < 0) {
+      if (++it.j < it.nt) return;
+      it.j = 0;
+    }
     if (++it.h < p.g.num_kv_heads) return;
     it.h = 0;
     int b = it.b + 1;
@@ -127,7 +137,7 @@ struct RowsWalk {
   }
   // its pages [j0, j1) that lie in units [u0, u1)
   __device__ __forceinline__ void piece(const RowsItem& it, int64_t u0, int64_t u1, int& j0, int& j1) const {
-    const int64_t f = it.u + p.setup, np = item_pages(it);
+    const int64_t f = it.u + p.setup, np = !LANES || it.j < it.nt ? item_pages(it) : 0;
     const int64_t a = u0 > f ? (u0 - f + kPage - 1) / kPage : 0, e = u1 > f ? (u1 - f + kPage - 1) / kPage : 0;
     j0 = static_cast<int>(a < np ? a : np);
     j1 = static_cast<int>(e < np ? e : np);
@@ -140,7 +150,7 @@ struct RowsWalk {
 struct __align__(16) RowsPiece {
   int row0, tok0, n, ctx;   // the request's first row, the item's first token, the request's tokens, positions before them
   int j0, j1, e0, e1;
-  int np, h, b, pad;        // the item's pages
+  int np, h, b, pad;        // the item's pages, KV head, request
   int64_t first, pad2;      // unit of its first page
 };
 constexpr int kRowsPieces = 4;   // pieces scheduled ahead
@@ -152,8 +162,10 @@ __device__ __forceinline__ int64_t rows_begin(int64_t c, int64_t W, int64_t P) {
   return W < (1 << 22) ? static_cast<uint32_t>(c * W) / static_cast<uint32_t>(P) : cta_unit_begin(c, W, P);
 }
 
-// Units of request b over all its items; 0 when it has none or is left out.
-__device__ __forceinline__ int64_t rows_units(const RowsAttnParams& p, int b, int toks, bool causal, bool flag) {
+// Units of request b over all its items, 0 when it has none or is left out;
+// `one`: of one item per KV head (trees: all items of a head cost the same).
+__device__ __forceinline__ int64_t rows_units(const RowsAttnParams& p, int b, int toks, bool causal, bool flag, int64_t& one) {
+  one = 0;
   const RowSpan s = row_span(p.g, b);
   if (!s.ok) {
     if (flag) atomicOr(p.g.err, TRTV_DEVERR_INDPTR);
@@ -166,39 +178,64 @@ __device__ __forceinline__ int64_t rows_units(const RowsAttnParams& p, int b, in
     return 0;
   }
   const int64_t nt = (s.n + toks - 1) / toks;
-  const int64_t head = causal ? nt * (p.setup + static_cast<int64_t>(L - s.n)) + toks * (nt * (nt + 1) / 2)
-                              : nt * (p.setup + static_cast<int64_t>(L));
-  return head * p.g.num_kv_heads;
+  one = (p.setup + static_cast<int64_t>(L)) * p.g.num_kv_heads;
+  return causal ? (nt * (p.setup + static_cast<int64_t>(L - s.n)) + toks * (nt * (nt + 1) / 2)) * p.g.num_kv_heads : nt * one;
 }
 
 // Exclusive scan of the requests' units into scan[0 .. batch]; the whole block.
-__device__ __forceinline__ void rows_scan(const RowsAttnParams& p, int toks, bool causal, int64_t* scan,
+// LANES: true, and the scan is of one item per head, where the CTAs in
+// `items` lanes, each with an item of every head, would be done at most a fifth
+// later than with all items in one row: the lanes' CTAs read a head's pages at
+// the same time, so that one read of HBM serves them.
+template <bool LANES>
+__device__ __forceinline__ bool rows_scan(const RowsAttnParams& p, int toks, bool causal, int items, int64_t* scan,
                                           int64_t* warp_tot) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, n = p.g.batch;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, n = p.g.batch, warps = nthr / 32;
   const int seg = (n + nthr - 1) / nthr, lo = min(n, tid * seg), hi = min(n, lo + seg);
-  int64_t local = 0;
+  int64_t all = 0, one = 0;
   for (int i = lo; i < hi; ++i) {
-    const int64_t c = rows_units(p, i, toks, causal, blockIdx.x == 0);
+    int64_t o;
+    const int64_t c = rows_units(p, i, toks, causal, blockIdx.x == 0, o);
     scan[i] = c;
-    local += c;
+    all += c;
+    one += o;
   }
-  int64_t incl = local;
+  int64_t incl = all, incl_one = one;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
   if (lane == 31) warp_tot[warp] = incl;
+  if constexpr (LANES) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl_one, o);
+      if (lane >= o) incl_one += v;
+    }
+    if (lane == 31) warp_tot[warps + warp] = incl_one;
+  }
   __syncthreads();
-  int64_t run = incl - local;
-  for (int w = 0; w < warp; ++w) run += warp_tot[w];
+  bool lanes = false;
+  if constexpr (LANES) {
+    int64_t w_all = 0, w_one = 0;
+    for (int w = 0; w < warps; ++w) {
+      w_all += warp_tot[w];
+      w_one += warp_tot[warps + w];
+    }
+    lanes = 5 * w_one * p.num_ctas <= 6 * w_all * (p.num_ctas / items);
+  }
+  int64_t run = lanes ? incl_one - one : incl - all;
+  for (int w = 0; w < warp; ++w) run += warp_tot[lanes ? warps + w : w];
   for (int i = lo; i < hi; ++i) {
-    const int64_t c = scan[i];
+    int64_t c = scan[i];
+    if (LANES && lanes) rows_units(p, i, toks, causal, false, c);
     scan[i] = run;
     run += c;
   }
   if (tid == nthr - 1) scan[n] = run;
   __syncthreads();
+  return lanes;
 }
 
 // ---- small device helpers -----------------------------------------------------
@@ -377,7 +414,7 @@ __device__ __forceinline__ void row_exp(uint32_t ts, int c, const uint32_t (&x)[
   tmem_st16(ts + 16 * c, o);
 }
 
-template <int D, bool FP8, bool TWO>
+template <int D, bool FP8, bool TWO, bool LANES>
 __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
     rows_attn_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
                      const __grid_constant__ RowsAttnParams p) {
@@ -456,13 +493,14 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
   }
   if (tid < kRowsTile) rowmap[tid] = make_ushort2(static_cast<unsigned short>(tid / g.group), static_cast<unsigned short>(tid % g.group));
   pdl_wait();   // inputs may come from the previous kernel of the stream
-  rows_scan(p, toks, causal, scan, scan + g.batch + 1);
+  const bool lanes = rows_scan<LANES>(p, toks, causal, LANES ? p.items : 1, scan, scan + g.batch + 1);
   pdl_trigger();
   const int64_t W = scan[g.batch];
   // little work is spread over fewer CTAs: pieces of less than kRowsLeast
   // positions cost more to join than they save
-  const int64_t P = max(int64_t{1}, min(static_cast<int64_t>(p.num_ctas), W / kRowsLeast));
-  const int64_t u0 = rows_begin(blockIdx.x, W, P), u1 = rows_begin(blockIdx.x + 1, W, P);
+  const int stride = LANES && lanes ? p.items : 1, rank = static_cast<int>(blockIdx.x) / stride;
+  const int64_t P = max(int64_t{1}, min(static_cast<int64_t>(p.num_ctas / stride), W / kRowsLeast));
+  const int64_t u0 = rows_begin(rank, W, P), u1 = rows_begin(rank + 1, W, P);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -569,7 +607,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
   } else if (warp == 11) {
     // ------------------------------------------------- schedule and Q loads
     // Q tiles: TWO: tile s in slot s; else one slot
-    const RowsWalk walk{p, scan, toks, causal};
+    const RowsWalk<LANES> walk{p, scan, toks, causal, LANES && lanes ? static_cast<int>(blockIdx.x) % stride : -1};
     RowsItem it = walk.at(u0, lane);
     if (lane == 0) {
       prefetch_tensormap(&q_map);
@@ -964,6 +1002,8 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         d.n = it.n;
         d.row0 = it.row0;
         d.c_last = static_cast<int>(cta_of_unit(it.first + static_cast<int64_t>(np - 1) * kPage, W, P));
+        if constexpr (LANES) d.c_last = d.c_last * stride + static_cast<int>(blockIdx.x) % stride;
+        d.stride = stride;
         p.splits[blockIdx.x] = d;
         split = true;
       }
@@ -1131,13 +1171,22 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
   }
 }
 
-template <int D, bool FP8, bool TWO>
+template <int D, bool FP8, bool TWO, bool LANES>
 cudaError_t launch_rows_attn_one(const CUtensorMap& kv_map, const CUtensorMap& q_map, const RowsAttnParams& p,
                                  size_t smem, cudaStream_t st) {
-  const void* fn = reinterpret_cast<const void*>(&rows_attn_kernel<D, FP8, TWO>);
+  const void* fn = reinterpret_cast<const void*>(&rows_attn_kernel<D, FP8, TWO, LANES>);
   const cudaError_t e = ensure_smem_attr(fn, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(rows_attn_kernel<D, FP8, TWO>, dim3(p.num_ctas), dim3(FP8 ? 512 : 384), smem, st, kv_map, q_map, p);
+  return launch_pdl(rows_attn_kernel<D, FP8, TWO, LANES>, dim3(p.num_ctas), dim3(FP8 ? 512 : 384), smem, st, kv_map, q_map, p);
+}
+
+// two: 256-row items, in `items` lanes where a tree has more than one a head
+template <int D, bool FP8>
+cudaError_t launch_rows_attn_kind(bool two, const CUtensorMap& kv_map, const CUtensorMap& q_map, const RowsAttnParams& p,
+                                  size_t smem, cudaStream_t st) {
+  if (!two) return launch_rows_attn_one<D, FP8, false, false>(kv_map, q_map, p, smem, st);
+  return p.items > 1 ? launch_rows_attn_one<D, FP8, true, true>(kv_map, q_map, p, smem, st)
+                     : launch_rows_attn_one<D, FP8, true, false>(kv_map, q_map, p, smem, st);
 }
 
 }  // namespace trtv

@@ -7,8 +7,7 @@ namespace trtv {
 
 cudaError_t launch_rows_attn_fp8(bool two, const CUtensorMap& kv_map, const CUtensorMap& q_map,
                                  const RowsAttnParams& p, size_t smem, cudaStream_t st) {
-  return two ? launch_rows_attn_one<128, true, true>(kv_map, q_map, p, smem, st)
-             : launch_rows_attn_one<128, true, false>(kv_map, q_map, p, smem, st);
+  return launch_rows_attn_kind<128, true>(two, kv_map, q_map, p, smem, st);
 }
 
 // Joins the pieces o_i (each normalised by its own sum, log2 lse_i) of a cut
@@ -28,10 +27,10 @@ __global__ void __launch_bounds__(kJoinThreads, 4) rows_join_kernel(const __grid
   const int c0 = blockIdx.x / (ROWS / kJoinRows), chunk = blockIdx.x % (ROWS / kJoinRows), tid = threadIdx.x;
   pdl_wait();
   pdl_trigger();
-  // b, h, tok0, n | row0, c_last
+  // b, h, tok0, n | row0, c_last, stride
   const int4 d0 = __ldcg(reinterpret_cast<const int4*>(p.splits + c0)), d1 = __ldcg(reinterpret_cast<const int4*>(p.splits + c0) + 1);
   if (d0.x < 0) return;
-  const int nc = d1.y - c0 + 1;
+  const int nc = (d1.y - c0) / d1.z + 1;
   float m[EL], l[EL];
   float4 acc[EL];
   int row[EL], tok[EL];
@@ -52,7 +51,7 @@ __global__ void __launch_bounds__(kJoinThreads, 4) rows_join_kernel(const __grid
     bool used[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int c = c0 + min(i0 + k, nc - 1);
+      const int c = c0 + min(i0 + k, nc - 1) * d1.z;
       used[k] = i0 + k < nc && (i0 + k == 0 || __ldcg(p.cont + c) != 0);
       const int64_t sl = 2 * static_cast<int64_t>(c) + (i0 + k == 0 ? 1 : 0);   // (an unused slot holds anything)
 #pragma unroll

@@ -194,6 +194,45 @@ def test_tree_split(num_ctas):
     check(p, p.tree(m), m)
 
 
+@pytest.mark.parametrize("num_ctas", [0, 1, 2, 3, 7, 152, 1024])
+@pytest.mark.parametrize("hq,hk,d,fp8", [(32, 4, 128, False), (16, 2, 64, False), (32, 4, 128, True)])
+def test_trees_of_several_items(num_ctas, hq, hk, d, fp8):
+    """More than 256 rows a KV head: the items of a head side by side on the CTAs (trees of equal size), or one
+    after the other (one large tree among small ones); empty and invalid requests among them."""
+    for new, ctx in (([64, 60, 64], [900, 2000, 3]), ([128], [700]), ([100, 0, 3, 2, 1, 5], [40, 9, 1500, 1000, 800, 0])):
+        p = Rows(new, ctx, hq, hk, d, fp8=fp8, num_ctas=num_ctas, pad=3, seed=len(new))
+        m = p.tree_masks("random")
+        check(p, p.tree(m), m)
+    p = Rows([64, 60, 64], [900, 2000, 3], hq, hk, d, fp8=fp8, num_ctas=num_ctas)
+    p.kv_lens[1] = 5
+    m = p.tree_masks()
+    out = p.tree(m, T.TRTV_F32)
+    torch.cuda.synchronize()
+    assert T.trtv_get_device_error() == T.DEVERR_KV_LEN and (out[64:124] == 0).all()
+    check(p, out, m, rows=slice(0, 64))
+    check(p, out, m, rows=slice(124, 188))
+
+
+def test_pages_past_32_bit_offsets():
+    """Slots whose pages lie beyond 2^32 bytes and 2^31 elements of the pool."""
+    p = Rows([40, 16], [200, 1000], 8, 2, 128)
+    slots = 1 << 14                                     # 2 x 64 KB each: 2 GiB ...
+    p.geom.num_slots, p.geom.slot_stride = slots, 5     # ... times 2.5
+    pool = torch.zeros(slots * 5, 4, 2, 32, 128, dtype=torch.bfloat16, device=p.dev)
+    assert pool.numel() > 1 << 31
+    table = p.table.clone()
+    for b in range(2):
+        for j in range((p.kv[b] + 127) // 128):
+            s, far = int(table[b, j]), slots - 1 - 7 * (16 * b + j)
+            pool[far * 5], pool[far * 5 + 1] = p.pool[s * 2], p.pool[s * 2 + 1]
+            p.table[b, j] = far
+    p.pool, p.stride, p.slots = pool, 5, slots
+    check(p, p.prompt())
+    p.geom.qo_len = p.qo_len = 40
+    m = p.tree_masks()
+    check(p, p.tree(m), m)
+
+
 # ---------------------------------------------------------------------------
 # device errors, streams, graphs
 
@@ -353,3 +392,52 @@ def test_a_turn():
                 m[t, t] = True
             masks.append(m)
         turn([12, 9], masks, paths)
+
+
+def test_binding_refusals():
+    """Tensors of another type, shape, device or layout are refused before anything runs."""
+    p = Rows([8, 4], [100, 20], 8, 2, 128)
+    ws, nb = p.workspace()
+    out = torch.zeros(p.rows, p.hq, p.d, dtype=torch.bfloat16, device=p.dev)
+    mask = pack(p.tree_masks(), p.qo_len)
+    good = dict(q=p.q, kv_pool=p.pool, page_table=p.table, kv_lens=p.kv_lens, qo_indptr=p.indptr, tree_mask=mask, out=out,
+                out_dtype=T.TRTV_BF16, workspace=ws, ws_bytes=nb)
+
+    def prompt(**over):
+        a = dict(good, **over)
+        a.pop("tree_mask")
+        T.trtv_prompt_attn(p.geom, **a)
+
+    def tree(**over):
+        T.trtv_verify_tree(p.geom, **dict(good, **over))
+
+    bad = dict(q=[p.q.float(), p.q[:, :4], p.q.cpu(), p.q.transpose(0, 1)], kv_pool=[p.pool[:-2], p.pool.float(), p.pool.cpu()],
+               page_table=[p.table.long(), p.table[:1], p.table.cpu()], kv_lens=[p.kv_lens.long(), p.kv_lens[:1]],
+               qo_indptr=[p.indptr[:-1], p.indptr.long()], out=[out[:-1], out.float(), out.cpu()],
+               workspace=[ws[:-1], ws.cpu()])
+    for name, values in bad.items():
+        for v in values:
+            for call in (prompt, tree):
+                with pytest.raises(ValueError, match=name):
+                    call(**{name: v})
+    for v in (mask.long(), mask[:-1], mask.cpu()):
+        with pytest.raises(ValueError, match="tree_mask"):
+            tree(tree_mask=v)
+    with pytest.raises(T.TrtvError):
+        prompt(ws_bytes=nb - 256)
+    path, plen, new = (torch.zeros(*s, dtype=torch.int32, device=p.dev) for s in ((2, 3), (2,), (2,)))
+    for a in ((path.long(), plen, new), (path[:1], plen, new), (path, plen[:1], new), (path, plen, new.cpu())):
+        with pytest.raises(ValueError):
+            T.trtv_tree_commit(p.geom, p.pool, p.table, p.kv_lens, p.indptr, *a)
+    k = torch.zeros(p.rows, 2, 128, dtype=torch.bfloat16, device=p.dev)
+    for a in ((p.q[:, :, :64], k, k), (p.q, k[:-1], k), (p.q, k, k.float()), (p.q, k.transpose(1, 2).contiguous().transpose(1, 2), k)):
+        with pytest.raises(ValueError):
+            T.trtv_norm_rope_stage(p.geom, *a, None, None, 0.0, None, 0, False, None, p.indptr, out, p.pool, p.table, p.kv_lens)
+    # nothing to do: no rows
+    empty = torch.zeros(3, dtype=torch.int32, device=p.dev)
+    none = torch.zeros(0, p.hq, p.d, dtype=torch.bfloat16, device=p.dev)
+    prompt(q=none, out=none, qo_indptr=empty)
+    T.trtv_norm_rope_stage(p.geom, none, k[:0], k[:0], None, None, 0.0, None, 0, False, None, empty, none, p.pool, p.table,
+                           p.kv_lens)
+    torch.cuda.synchronize()
+    assert T.trtv_get_device_error() == 0

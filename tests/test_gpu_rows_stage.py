@@ -277,6 +277,37 @@ def test_commit_device_errors():
     both(length(1 << 20), T.DEVERR_KV_LEN)
 
 
+def test_stage_and_commit_past_32_bit_offsets():
+    """A pool of more than 2^31 elements, its last slots used."""
+    p = Rows([6, 3], [125, 40], 4, 2, 128)
+    slots = 1 << 14
+    pool = torch.zeros(slots * 5, 4, 2, 32, 128, dtype=torch.bfloat16, device=p.dev)
+    assert pool.numel() > 1 << 31
+    for b in range(2):
+        for j in range((p.kv[b] + 127) // 128):
+            p.table[b, j] = slots - 1 - 3 * (2 * b + j)
+    p.pool, p.stride, p.slots = pool, 5, slots
+    p.geom.num_slots, p.geom.slot_stride = slots, 5
+    q, k, v, w = inputs(p)
+    out = torch.empty(p.rows, p.hq, p.d, dtype=torch.bfloat16, device=p.dev)
+    T.trtv_norm_rope_stage(p.geom, q, k, v, None, None, 0.0, None, 0, False, None, p.indptr, out, p.pool, p.table, p.kv_lens)
+    req, cell = place(p)
+    buf = p.table.long()[req, cell // 128] * 5
+    got = pool[buf, cell % 128 // 32, :, cell % 32]
+    assert torch.equal(out, q) and torch.equal(got, k)
+    assert torch.equal(pool[buf + 1, cell % 128 // 32, :, cell % 32], v)
+    new = commit(p, [[0, 3, 5], [2]])
+    assert new.tolist() == [128, 41] and T.trtv_get_device_error() == 0
+    for b, path in ((0, [0, 3, 5]), (1, [2])):
+        for i, t in enumerate(path):
+            pos = p.ctx[b] + i
+            at = int(p.table[b, pos // 128]) * 5
+            row = p.start(b) + t
+            assert torch.equal(pool[at, pos % 128 // 32, :, pos % 32], k[row])
+            assert torch.equal(pool[at + 1, pos % 128 // 32, :, pos % 32], v[row])
+    assert (pool != 0).any(-1).sum().item() <= 2 * 2 * 9
+
+
 def test_calls_in_a_graph_and_on_another_stream():
     """Staging and commit captured once and replayed with lengths changed on the device."""
     p = Rows([4, 9], [10, 300], 8, 2, 128, extra_pages=2)

@@ -15,9 +15,9 @@ namespace {
 constexpr int kMaxBatch = 2048;   // the requests' scan lies in shared memory
 constexpr int kMaxTreeTokens = 128;
 // stream-K charge of an item in positions: what switching items costs (16384-token
-// prompt 1581 / 1518 / 1467 / 1471 us at 128 / 256 / 384 / 512, packed prompts 639 /
-// 550 / 522 / 532; one-tile items 169 / 171 / 172 us at 128 / 256 / 384)
-constexpr int kRowsSetupTwo = 384, kRowsSetupOne = 128;
+// prompt 1581 / 1518 / 1467 / 1471 us at 128 / 256 / 384 / 512, over E4M3 1725 /
+// 1675 / 1683 at 384 / 512 / 640; one-tile items 169 / 171 / 172 us at 128 / 256 / 384)
+constexpr int kRowsSetupTwo = 384, kRowsSetupTwoFp8 = 512, kRowsSetupOne = 128;
 
 // Geometry checks shared by the packed-row calls.
 trtv_status rows_geom(const trtv_geom* g, const int32_t* indptr, int32_t num_tokens, RowsGeom* r) {
@@ -201,7 +201,7 @@ trtv_status rows_attn(const trtv_geom* g, const void* q, const void* pool, const
   p.cont = reinterpret_cast<int*>(wsb + pl.ws_cont);
   p.out_f32 = out_dtype == TRTV_F32;
   p.num_ctas = pl.num_ctas;
-  p.setup = pl.two ? kRowsSetupTwo : kRowsSetupOne;
+  p.setup = !pl.two ? kRowsSetupOne : g->kv_dtype == TRTV_FP8_E4M3 ? kRowsSetupTwoFp8 : kRowsSetupTwo;
   p.scale_log2 = g->sm_scale * g->k_scale * 1.4426950408889634f;
   p.v_scale = g->v_scale;
   p.wait_ns = wait_limit_ns();

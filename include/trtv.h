@@ -368,7 +368,8 @@ trtv_status trtv_draft_attn_p32(const trtv_geom* geom, const void* q, const void
  * kv_len counts the new tokens: token t of request b is cache position
  * c_b + t with c_b = kv_len[b] - n_b.  A request with n_b = 0 takes no part
  * (its length is not checked).  head_dim 64 or 128 (FP8 caches: 128),
- * num_q_heads / num_kv_heads <= 128, batch <= 2048.
+ * num_q_heads / num_kv_heads <= 128, num_q_heads <= 65536, batch <= 2048,
+ * sm_scale * k_scale >= 2^-64.
  * A request whose qo_indptr entries are not ascending within
  * [0, num_tokens], or give more than qo_len tokens, is left out
  * (TRTV_DEVERR_INDPTR); one with kv_len < n_b or beyond 128 * max_pages_per_req

@@ -14,6 +14,8 @@ namespace {
 
 constexpr int kMaxBatch = 2048;   // the requests' scan lies in shared memory
 constexpr int kMaxTreeTokens = 128;
+constexpr int kMaxHeads = 65536;  // a token's row is indexed by 32 bits
+constexpr float kMinScale = 5.421011e-20f;  // 2^-64
 // stream-K charge of an item in positions: what switching items costs (16384-token
 // prompt 1581 / 1518 / 1467 / 1471 us at 128 / 256 / 384 / 512, over E4M3 1725 /
 // 1675 / 1683 at 384 / 512 / 640; one-tile items 169 / 171 / 172 us at 128 / 256 / 384)
@@ -30,9 +32,12 @@ trtv_status rows_geom(const trtv_geom* g, const int32_t* indptr, int32_t num_tok
   if (!(g->sm_scale > 0.f) || !(g->k_scale > 0.f) || !std::isfinite(g->sm_scale) || !std::isfinite(g->k_scale) ||
       !std::isfinite(g->v_scale))
     return TRTV_ERR_INVALID_ARG;
+  // (a scale that vanishes in binary32 would turn a masked score of minus infinity into NaN)
+  if (!(g->sm_scale * g->k_scale >= kMinScale) || !std::isfinite(g->sm_scale * g->k_scale)) return TRTV_ERR_INVALID_ARG;
   if (g->head_dim != 64 && g->head_dim != 128) return TRTV_ERR_UNSUPPORTED;
   if (g->kv_dtype == TRTV_FP8_E4M3 && g->head_dim != 128) return TRTV_ERR_UNSUPPORTED;
-  if (g->batch > kMaxBatch || g->num_q_heads / g->num_kv_heads > 128) return TRTV_ERR_UNSUPPORTED;
+  if (g->batch > kMaxBatch || g->num_q_heads > kMaxHeads || g->num_q_heads / g->num_kv_heads > 128)
+    return TRTV_ERR_UNSUPPORTED;
   // cache positions are 32-bit, and the pool is addressed by 32-bit rows
   if (g->max_pages_per_req > (1 << 23)) return TRTV_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(g->num_slots) * g->slot_stride * kGroups * g->num_kv_heads * kSub >= (int64_t{1} << 31))
@@ -299,7 +304,7 @@ trtv_status trtv_verify_tree(const trtv_geom* g, const void* q, const void* kv_p
                              const int32_t* kv_lens, const int32_t* qo_indptr, int32_t num_tokens,
                              const uint32_t* tree_mask, void* out, int32_t out_dtype, void* workspace,
                              size_t ws_bytes, void* stream) {
-  if (tree_mask == nullptr) return TRTV_ERR_INVALID_ARG;
+  if (tree_mask == nullptr && num_tokens != 0) return TRTV_ERR_INVALID_ARG;
   if (g != nullptr && g->qo_len > kMaxTreeTokens) return TRTV_ERR_UNSUPPORTED;
   return rows_attn(g, q, kv_pool, page_table, kv_lens, qo_indptr, num_tokens, tree_mask, out, out_dtype, workspace,
                    ws_bytes, stream);

@@ -881,7 +881,8 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
             for (int k = 0; k < 4; ++k)
               amax = max3(amax, fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u)));
           }
-          const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
+          // (rows below 2^-40 are taken as 2^-40: the scale stays a normal number)
+          const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -40);
           const float mul = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
           scale *= __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
           if (!TWO) named_barrier(1, 256);

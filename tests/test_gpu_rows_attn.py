@@ -441,3 +441,53 @@ def test_binding_refusals():
                            p.kv_lens)
     torch.cuda.synchronize()
     assert T.trtv_get_device_error() == 0
+
+
+@pytest.mark.parametrize("hq,hk,d,fp8", [(32, 4, 128, False), (32, 4, 128, True), (8, 2, 64, False), (2, 2, 128, False),
+                                         (2, 2, 128, True)])
+@pytest.mark.parametrize("call", ["prompt", "tree"])
+def test_other_rows_of_a_tile_may_hold_anything(call, hq, hk, d, fp8):
+    """Tiles reach past a request's rows into the next request's, and past the last request's: NaN there stays there."""
+    p = Rows([37, 5, 3, 90], [100, 0, 300, 10], hq, hk, d, fp8=fp8, pad=40, seed=3)
+    m = p.tree_masks()
+    clean = p.prompt() if call == "prompt" else p.tree(m)
+    p.q[37:42] = math.nan
+    p.q[135:] = math.inf
+    out = p.prompt() if call == "prompt" else p.tree(m)
+    torch.cuda.synchronize()
+    assert T.trtv_get_device_error() == 0
+    assert torch.equal(out[:37], clean[:37]) and torch.equal(out[42:], clean[42:])
+    assert not torch.isfinite(out[37:42]).any()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_rows_of_zeros_and_tiny_scales(fp8):
+    """Queries of zeros or far below one weigh every position they see alike, with a softmax scale that leaves the
+    logits at zero as well."""
+    for scale in (None, 1e-9, 1e-15):
+        p = Rows([150, 3], [70, 0], 8, 2, 128, fp8=fp8, seed=6)
+        if scale is not None:
+            p.geom.sm_scale = scale
+        p.q[0:50] = 0
+        p.q[50:60] *= 2.0 ** -60
+        p.q[60:62] *= 2.0 ** -110
+        p.q[150:] = 0
+        check(p, p.prompt())
+        p = Rows([50, 3], [70, 0], 8, 2, 128, fp8=fp8, seed=7)
+        if scale is not None:
+            p.geom.sm_scale = scale
+        p.q[0:30] = 0
+        m = p.tree_masks("random")
+        check(p, p.tree(m), m)
+
+
+def test_a_step_without_tokens():
+    p = Rows([3], [4], 8, 2, 128)
+    empty = torch.zeros(2, dtype=torch.int32, device=p.dev)
+    q = torch.empty(0, 8, 128, dtype=torch.bfloat16, device=p.dev)
+    ws, nb = p.workspace()
+    mask = torch.empty(0, 1, dtype=torch.int32, device=p.dev)
+    T.trtv_prompt_attn(p.geom, q, p.pool, p.table, p.kv_lens, empty, torch.empty_like(q), T.TRTV_BF16, ws, nb)
+    T.trtv_verify_tree(p.geom, q, p.pool, p.table, p.kv_lens, empty, mask, torch.empty_like(q), T.TRTV_BF16, ws, nb)
+    torch.cuda.synchronize()
+    assert T.trtv_get_device_error() == 0

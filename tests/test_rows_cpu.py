@@ -41,7 +41,8 @@ def calls(lib, g, rows=80, indptr=16):
     (dict(num_ctas=-1), INVALID), (dict(num_ctas=1025), INVALID), (dict(head_dim=96), UNSUPPORTED),
     (dict(kv_dtype=1, head_dim=64), UNSUPPORTED), (dict(batch=2049), UNSUPPORTED),
     (dict(num_q_heads=129, num_kv_heads=1), UNSUPPORTED), (dict(num_slots=1 << 20, slot_stride=8), UNSUPPORTED),
-    (dict(max_pages_per_req=(1 << 23) + 1), UNSUPPORTED),
+    (dict(max_pages_per_req=(1 << 23) + 1), UNSUPPORTED), (dict(num_q_heads=65664, num_kv_heads=513), UNSUPPORTED),
+    (dict(sm_scale=1e-20), INVALID), (dict(sm_scale=1e-12, k_scale=1e-12), INVALID), (dict(sm_scale=1e30, k_scale=1e30), INVALID),
 ])
 def test_geometry(lib, over, status):
     g = geom(**over)
@@ -122,3 +123,11 @@ def test_commit_arguments(lib):
     a = list(good)
     a[0] = ctypes.byref(geom(qo_len=129))
     assert lib.trtv_tree_commit(*a) == UNSUPPORTED
+
+
+def test_no_rows_no_buffers(lib):
+    """A step without new tokens: empty tensors have no address."""
+    r = ctypes.byref(geom())
+    assert lib.trtv_verify_tree(r, None, None, None, None, 16, 0, None, None, 0, None, 0, None) == 0
+    assert lib.trtv_prompt_attn(r, None, None, None, None, 16, 0, None, 0, None, 0, None) == 0
+    assert lib.trtv_verify_tree(r, 16, 16, 16, 16, 16, -1, None, 16, 0, 256, 1 << 40, None) == INVALID

@@ -21,9 +21,12 @@ namespace trtv {
 // token's heads (q, then k, then v) in batches of kStageRows rows per lane
 // group, the next batch's loads out before this one is worked on; what a token
 // costs besides (its request, its page, its table row) is loaded once.
-// Bound by the bytes: 12 prompts of 13.6 k tokens, 72 heads of 128: 177 us =
-// 6.1 TB/s, 89 % of the copy rate (8 heads a warp and no look-ahead: 294 us;
-// batches of 1 / 3 / 4 rows: 203 / 185 / 195 us; blocks of 256 threads: 189 us).
+// Bound by the bytes: 12 prompts, 72 heads of 128, 1.07 GB: 176 us = 6.1 TB/s,
+// 90 % of the copy rate (8 heads a warp and no look-ahead: 294 us; batches of
+// 1 / 3 / 4 rows: 203 / 185 / 195 us; blocks of 256 threads: 189 us).  An E4M3
+// cache and fewer tokens (192 MB, 40 heads): 41.7 us = 68 %, two instruction
+// issues in three taken (pairing chosen at run time: 43.1 us; a branch per kind
+// of head instead of selects: 50 us, the rows' latencies no longer overlap).
 constexpr int kStageThreads = 128;
 constexpr int kStageRows = 2;   // rows in flight per lane group, twice
 
@@ -39,14 +42,12 @@ __device__ __forceinline__ uint2 pack4(const float (&x)[4]) {
 }
 
 __device__ __forceinline__ uint32_t pack4_e4m3(const float (&x)[4], float scale) {
-  uint32_t o = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    o |= static_cast<uint32_t>(__nv_cvt_float_to_fp8(x[i] / scale, __NV_SATFINITE, __NV_E4M3)) << (8 * i);
-  return o;
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[0] / scale, x[1] / scale), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[2] / scale, x[3] / scale), __NV_SATFINITE, __NV_E4M3);
+  return lo | (hi << 16);
 }
 
-template <int D, bool FP8>
+template <int D, bool FP8, bool INTER>
 __global__ void __launch_bounds__(kStageThreads) norm_rope_stage_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr int LPR = D / 8;         // lanes per row
   constexpr int GPW = 32 / LPR;      // rows a warp holds at a time
@@ -61,7 +62,7 @@ __global__ void __launch_bounds__(kStageThreads) norm_rope_stage_kernel(const __
   const int tok = static_cast<int>(unit / p.chunks);
   const int h0 = static_cast<int>(unit % p.chunks) * p.heads_per_warp, h1 = min(heads, h0 + p.heads_per_warp);
   const bool turns = 8 * l < p.rot_dim;
-  const bool halves = turns && !p.interleaved;
+  const bool halves = turns && !INTER;
   const int da = halves ? 4 * l : 8 * l, db = halves ? p.rot_dim / 2 + 4 * l : 8 * l + 4;
 
   // row h of the token's heads (q, then k, then v): bases such that row h lies h D on
@@ -154,14 +155,14 @@ __global__ void __launch_bounds__(kStageThreads) norm_rope_stage_kernel(const __
             c[i] = c[i] * f * wc[i];
           }
         }
-        if (halves) {
+        if (!INTER && turns) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float u = a[i] * co[i] - c[i] * si[i];
             c[i] = c[i] * co[i] + a[i] * si[i];
             a[i] = u;
           }
-        } else if (turns) {
+        } else if (INTER && turns) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float u = a[2 * i] * co[i] - a[2 * i + 1] * si[i];
@@ -205,9 +206,14 @@ cudaError_t launch_norm_rope_stage(int head_dim, bool fp8, const NormRopeParams&
   const int64_t warps = static_cast<int64_t>(p.chunks) * p.g.num_tokens;
   const int64_t blocks = (warps + kStageThreads / 32 - 1) / (kStageThreads / 32);
   const dim3 grid(static_cast<unsigned>(blocks)), block(kStageThreads);
-  if (fp8) return launch_pdl(norm_rope_stage_kernel<128, true>, grid, block, 0, st, p);
-  return head_dim == 64 ? launch_pdl(norm_rope_stage_kernel<64, false>, grid, block, 0, st, p)
-                        : launch_pdl(norm_rope_stage_kernel<128, false>, grid, block, 0, st, p);
+  if (p.interleaved) {
+    if (fp8) return launch_pdl(norm_rope_stage_kernel<128, true, true>, grid, block, 0, st, p);
+    return head_dim == 64 ? launch_pdl(norm_rope_stage_kernel<64, false, true>, grid, block, 0, st, p)
+                          : launch_pdl(norm_rope_stage_kernel<128, false, true>, grid, block, 0, st, p);
+  }
+  if (fp8) return launch_pdl(norm_rope_stage_kernel<128, true, false>, grid, block, 0, st, p);
+  return head_dim == 64 ? launch_pdl(norm_rope_stage_kernel<64, false, false>, grid, block, 0, st, p)
+                        : launch_pdl(norm_rope_stage_kernel<128, false, false>, grid, block, 0, st, p);
 }
 
 // ---------------------------------------------------------------------------

@@ -16,10 +16,14 @@ constexpr int kMaxBatch = 2048;   // the requests' scan lies in shared memory
 constexpr int kMaxTreeTokens = 128;
 constexpr int kMaxHeads = 65536;  // a token's row is indexed by 32 bits
 constexpr float kMinScale = 5.421011e-20f;  // 2^-64
-// stream-K charge of an item in positions: what switching items costs (16384-token
-// prompt 1581 / 1518 / 1467 / 1471 us at 128 / 256 / 384 / 512, over E4M3 1725 /
-// 1675 / 1683 at 384 / 512 / 640; one-tile items 169 / 171 / 172 us at 128 / 256 / 384)
-constexpr int kRowsSetupTwo = 384, kRowsSetupTwoFp8 = 512, kRowsSetupOne = 128;
+// stream-K charge of an item in positions, what switching items costs.  256-row
+// items, bf16: 8 prompts of up to 4000 tokens 459 / 435 / 439 / 450 / 455 us at
+// 192 / 256 / 320 / 384 / 512; E4M3: a prompt of 16384 1674 / 1626 / 1635 / 1647 at
+// 384 / 448 / 512 / 640, 4 chunks over 2-12 k positions 148.0 / 147.5 / 146.7 /
+// 146.5.  One tile: 64 trees of 16 nodes 108.2 / 106.7 / 105.7 / 104.4 at 64 / 96 /
+// 128 / 256, but one tree of 8 over 900 positions is cut best at 128; over E4M3 112.9
+// / 111.5 / 110.5 / 105.8.
+constexpr int kRowsSetupTwo = 256, kRowsSetupTwoFp8 = 512, kRowsSetupOne = 128, kRowsSetupOneFp8 = 256;
 
 // Geometry checks shared by the packed-row calls.
 trtv_status rows_geom(const trtv_geom* g, const int32_t* indptr, int32_t num_tokens, RowsGeom* r) {
@@ -97,23 +101,21 @@ bool rows_plan(const trtv_geom* g, const RowsGeom& r, RowsPlan* pl) {
 }
 
 // Shared memory: Q (one or two tiles), the page ring, E4M3: the codes' ring, the
-// groups' exchange, the output rows' staging, the
-// pieces, the requests' scan and its 32 warp totals, barriers.  The ring takes what is left,
-// at most kMaxStages pages.
+// groups' exchange, the pieces, the requests' scan and its 32 warp totals,
+// barriers.  The ring takes what is left, at most kMaxStages pages.
 constexpr int kMaxStages = 8;
 bool rows_smem(const trtv_geom* g, const RowsPlan& pl, RowsAttnParams* p, size_t* bytes) {
   const bool fp8 = g->kv_dtype == TRTV_FP8_E4M3;
   const size_t tile = static_cast<size_t>(kRowsTile) * g->head_dim * 2, raw = static_cast<size_t>(kRowsTile) * g->head_dim;
   const size_t scan = align_up((static_cast<size_t>(g->batch) + 1 + 32) * sizeof(int64_t), 16);
   const size_t ml = pl.two ? 0 : 2 * kRowsTile * 2 * sizeof(float);
-  const size_t bars = (4 * kMaxStages + 32) * sizeof(uint64_t), pieces = 4 * 64, rowmap = kRowsTile * 4;
-  const size_t stage = static_cast<size_t>(8) * 32 * rows_segment(fp8);
+  const size_t bars = (4 * kMaxStages + 32) * sizeof(uint64_t), pieces = 4 * 48;
   const size_t q = (pl.two ? 2 : 1) * tile;
-  const size_t fixed = q + ml + stage + rowmap + pieces + scan + bars + kAlignSlack;
+  const size_t fixed = q + ml + pieces + scan + bars + kAlignSlack;
   if (fp8) {
     // four converted tiles and three stages of codes where they fit (one-tile
-    // items: 133 us against 143 with three and five, 64 trees of 16 nodes), else
-    // three; what is left holds codes in flight
+    // items, 64 trees of 16 nodes: 7 % faster than three and five), else three;
+    // what is left holds codes in flight
     if (fixed + 2 * raw + 3 * tile > kSmemOptin) return false;
     p->nst = fixed + 3 * raw + 4 * tile <= kSmemOptin ? 4 : 3;
     p->nraw = static_cast<int>(std::min<size_t>((kSmemOptin - fixed - p->nst * tile) / raw, kMaxStages));
@@ -132,10 +134,6 @@ bool rows_smem(const trtv_geom* g, const RowsPlan& pl, RowsAttnParams* p, size_t
   off += codes;
   p->off_ml = static_cast<int>(off);
   off += ml;
-  p->off_stage = static_cast<int>(off);
-  off += stage;
-  p->off_rowmap = static_cast<int>(off);
-  off += rowmap;
   p->off_pieces = static_cast<int>(off);
   off += pieces;
   p->off_scan = static_cast<int>(off);
@@ -206,14 +204,15 @@ trtv_status rows_attn(const trtv_geom* g, const void* q, const void* pool, const
   p.cont = reinterpret_cast<int*>(wsb + pl.ws_cont);
   p.out_f32 = out_dtype == TRTV_F32;
   p.num_ctas = pl.num_ctas;
-  p.setup = !pl.two ? kRowsSetupOne : g->kv_dtype == TRTV_FP8_E4M3 ? kRowsSetupTwoFp8 : kRowsSetupTwo;
+  const bool fp8 = g->kv_dtype == TRTV_FP8_E4M3;
+  p.setup = pl.two ? (fp8 ? kRowsSetupTwoFp8 : kRowsSetupTwo) : fp8 ? kRowsSetupOneFp8 : kRowsSetupOne;
   p.scale_log2 = g->sm_scale * g->k_scale * 1.4426950408889634f;
   p.v_scale = g->v_scale;
   p.wait_ns = wait_limit_ns();
   p.withhold = withheld_pages();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = g->kv_dtype == TRTV_FP8_E4M3 ? launch_rows_attn_fp8(pl.two, kv_map, q_map, p, smem, st)
-                                               : launch_rows_attn_bf16(g->head_dim, pl.two, kv_map, q_map, p, smem, st);
+  cudaError_t e = fp8 ? launch_rows_attn_fp8(pl.two, kv_map, q_map, p, smem, st)
+                      : launch_rows_attn_bf16(g->head_dim, pl.two, kv_map, q_map, p, smem, st);
   if (e == cudaSuccess) e = launch_rows_join(g->head_dim, pl.two, p, st);
   return e == cudaSuccess ? TRTV_OK : TRTV_ERR_CUDA;
 }

@@ -89,9 +89,6 @@ struct CommitParams {
 };
 
 constexpr int kRowsTile = 128;   // rows of one UMMA tile of the attention
-// bytes of an output row that a softmax warp stages at a time (E4M3 caches
-// need the shared memory for their codes)
-__host__ __device__ constexpr int rows_segment(bool fp8) { return fp8 ? 32 : 64; }
 
 // A row-tile item of the attention that the stream-K split cut: written by the
 // CTA that holds its first page, read by the join kernel.
@@ -112,7 +109,7 @@ struct RowsAttnParams {
   int tile_toks;               // tokens of a 128-row tile: 128 / group
   int items;                   // trees: 256-row items that the largest has per KV head; else 1
   int nst, nraw;               // page stages in shared memory; FP8: stages of raw codes
-  int off_q, off_ring, off_raw, off_ml, off_stage, off_rowmap, off_pieces, off_scan, off_bar;   // shared memory, from the 1024-aligned base
+  int off_q, off_ring, off_raw, off_ml, off_pieces, off_scan, off_bar;   // shared memory, from the 1024-aligned base
   int setup;                   // what starting an item costs, in positions
   float scale_log2, v_scale;   // sm_scale * k_scale * log2(e)
   uint64_t wait_ns;

@@ -16,7 +16,7 @@
 // first position).  Pieces of an item cut between CTAs are joined by
 // rows_join_kernel.  LANES: a tree of more than 256 rows has several items a KV
 // head that read the same pages; the CTAs walk in as many lanes, abreast (see
-// rows_scan; 16 trees of 512 rows over 16-32 k positions: 320 -> 301 us).
+// rows_scan; 16 trees of 512 rows over 16-32 k positions: 6 % faster).
 //
 // Per page and tile: S = Q K^T (128 x 128, fp32 in TMEM), softmax in registers
 // (running maximum, moved only when it rises by more than 2^8; sums in fp32 of
@@ -40,8 +40,8 @@
 //
 // Warps: 0-3 and 4-7 softmax groups, 8 page loads, 9 (TWO: and 10) UMMA issue
 // (V rows at or past kv_len are zeroed first: P is zero there but 0 * NaN
-// is not), 11 the CTA's schedule (its pieces, a few ahead, in shared memory) and
-// Q loads, 12-15 (E4M3) conversion.
+// is not), 11 the CTA's schedule (its pieces, a few ahead, in shared memory; what
+// the join needs) and Q loads, 12-15 (E4M3) conversion.
 #pragma once
 
 #include "rows.cuh"
@@ -151,7 +151,6 @@ struct __align__(16) RowsPiece {
   int row0, tok0, n, ctx;   // the request's first row, the item's first token, the request's tokens, positions before them
   int j0, j1, e0, e1;
   int np, h, b, pad;        // the item's pages, KV head, request
-  int64_t first, pad2;      // unit of its first page
 };
 constexpr int kRowsPieces = 4;   // pieces scheduled ahead
 
@@ -401,17 +400,34 @@ __device__ __forceinline__ float row_max(const uint32_t (&x)[32]) {
 template <bool F16>
 __device__ __forceinline__ void row_exp(uint32_t ts, int c, const uint32_t (&x)[32], float scale, float negm, float2& sum) {
   const float2 sc2 = make_float2(scale, scale), ng2 = make_float2(negm, negm);
-  uint32_t o[16];
+  constexpr int N = F16 ? 8 : 16;   // pairs at a time (E4M3 kernels have fewer registers)
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    float2 v = make_float2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1]));
-    v = __ffma2_rn(v, sc2, ng2);
-    v.x = fast_exp2(v.x);
-    v.y = fast_exp2(v.y);
-    sum = __fadd2_rn(sum, v);
-    o[k] = pack2<F16>(v.x, v.y);
+  for (int h = 0; h < 16; h += N) {
+    uint32_t o[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      float2 v = make_float2(__uint_as_float(x[2 * (h + k)]), __uint_as_float(x[2 * (h + k) + 1]));
+      v = __ffma2_rn(v, sc2, ng2);
+      v.x = fast_exp2(v.x);
+      v.y = fast_exp2(v.y);
+      sum = __fadd2_rn(sum, v);
+      o[k] = pack2<F16>(v.x, v.y);
+    }
+    if constexpr (F16) tmem_st8(ts + 16 * c + h, o);
+    else tmem_st16(ts + 16 * c, o);
   }
-  tmem_st16(ts + 16 * c, o);
+}
+
+// 32 bytes to 16-byte aligned memory; `wide`: it is 32-byte aligned
+__device__ __forceinline__ void store_sector(uint8_t* dst, bool wide, const uint32_t (&w)[8]) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(dst + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 
 template <int D, bool FP8, bool TWO, bool LANES>
@@ -452,7 +468,6 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
   const Waits wt{g.err, abortf, p.wait_ns};
   int64_t* scan = reinterpret_cast<int64_t*>(smem + p.off_scan);
   float2* xml = reinterpret_cast<float2*>(smem + p.off_ml);        // [2 groups][128 rows] {reference maximum, sum}
-  ushort2* rowmap = reinterpret_cast<ushort2*>(smem + p.off_rowmap);   // [128] {token of the tile, head of the group}
   RowsPiece* pieces = reinterpret_cast<RowsPiece*>(smem + p.off_pieces);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool causal = p.tree_mask == nullptr;
@@ -491,7 +506,6 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
     tmem_alloc(tslot, 512);
     tmem_relinquish();
   }
-  if (tid < kRowsTile) rowmap[tid] = make_ushort2(static_cast<unsigned short>(tid / g.group), static_cast<unsigned short>(tid % g.group));
   pdl_wait();   // inputs may come from the previous kernel of the stream
   const bool lanes = rows_scan<LANES>(p, toks, causal, LANES ? p.items : 1, scan, scan + g.batch + 1);
   pdl_trigger();
@@ -499,7 +513,11 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
   // little work is spread over fewer CTAs: pieces of less than kRowsLeast
   // positions cost more to join than they save
   const int stride = LANES && lanes ? p.items : 1, rank = static_cast<int>(blockIdx.x) / stride;
-  const int64_t P = max(int64_t{1}, min(static_cast<int64_t>(p.num_ctas / stride), W / kRowsLeast));
+  // (a multiple of the KV heads: one request's heads are then all cut alike, no CTA
+  // has the end of one and the start of the next; a tree of 8 over 900 positions
+  // 14.0 us, 17.5 on 15 or 18 CTAs)
+  int64_t P = max(int64_t{1}, min(static_cast<int64_t>(p.num_ctas / stride), W / kRowsLeast));
+  if (P < p.num_ctas / stride && P > g.num_kv_heads) P -= static_cast<int>(P) % g.num_kv_heads;
   const int64_t u0 = rows_begin(rank, W, P), u1 = rows_begin(rank + 1, W, P);
   tc_fence_before();
   __syncthreads();
@@ -613,7 +631,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
       prefetch_tensormap(&q_map);
       const uint32_t bytes = static_cast<uint32_t>(p.tile_toks * g.group * D * 2);
       int used[2] = {0, 0};
-      bool ok = true;
+      bool ok = true, split = false;   // split: this CTA holds the first page of a cut item
       int seq = 0;
       for (;;) {
         RowsPiece x{};
@@ -630,7 +648,6 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           x.np = walk.item_pages(it);
           x.h = it.h;
           x.b = it.b;
-          x.first = it.u + p.setup;
           x.e0 = x.e1 = x.j1;
           if (TWO) {   // the tiles' own ends: the second may be empty, the first see fewer pages
             x.e0 = min(x.j1, walk.pages(it, x.tok0 + p.tile_toks));
@@ -656,9 +673,26 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
                        x.row0 + x.tok0 + s * p.tile_toks);
         }
         if (!ok) break;
+        // what the join needs to know
+        if (seq == 0) p.cont[blockIdx.x] = x.j0 > 0;
+        if (x.j0 == 0 && x.j1 < x.np) {
+          RowsSplit d{};
+          d.b = x.b;
+          d.h = x.h;
+          d.tok0 = x.tok0;
+          d.n = x.n;
+          d.row0 = x.row0;
+          d.c_last = static_cast<int>(cta_of_unit(it.u + p.setup + static_cast<int64_t>(x.np - 1) * kPage, W, P));
+          if constexpr (LANES) d.c_last = d.c_last * stride + static_cast<int>(blockIdx.x) % stride;
+          d.stride = stride;
+          p.splits[blockIdx.x] = d;
+          split = true;
+        }
         ++seq;
         walk.next(it);
       }
+      if (!split) p.splits[blockIdx.x].b = -1;
+      if (seq == 0) p.cont[blockIdx.x] = 0;   // no page starts in its units
       for (int s = 0; s < 2; ++s)
         if (used[s] > 0) mbar_drain(&qfull[s], static_cast<uint32_t>(used[s] - 1) & 1u, wt);
     }
@@ -849,7 +883,6 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
     };
     uint32_t sph = 0, oph = 0, qph = 0;             // parities of sfull[s]; odone[], qfull[] (bits)
     int seq = 0;
-    bool split = false;                             // this CTA holds the first page of a cut item
     // The piece stays in shared memory until its end (registers hold scores).
     for (;; ++seq) {
       const RowsPiece& it = pieces[seq % kRowsPieces];
@@ -866,14 +899,15 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
       if constexpr (FP8) {
         // Q row -> f16, scaled by a power of two that brings its largest
         // magnitude to [2^14, 2^15).  Where both groups read one tile, both
-        // look at the whole row, then convert a half each.
+        // look at the whole row, then convert a half each.  (Loops kept short:
+        // unrolled by four, 4 chunks of 1600 tokens take 688 us against 595.)
         const int slot = TWO ? s : 0;
         if (!TWO || je > it.j0) {
           wait_all(&qfull[slot], (qph >> slot) & 1u);
           qph ^= 1u << slot;
           uint8_t* row = qbase + slot * TILE + r * 128;
           float amax = 0.f;
-#pragma unroll 4
+#pragma unroll 2
           for (int c = 0; c < 16; ++c) {
             const uint4 v = *reinterpret_cast<const uint4*>(row + (c >> 3) * (TILE / 2) + (((c & 7) ^ (r & 7)) << 4));
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -886,7 +920,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           const float mul = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
           scale *= __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
           if (!TWO) named_barrier(1, 256);
-#pragma unroll 4
+#pragma unroll 1
           for (int c0 = 0; c0 < (TWO ? 16 : 8); ++c0) {
             const int c = TWO ? c0 : s * 8 + c0;
             uint4* q4 = reinterpret_cast<uint4*>(row + (c >> 3) * (TILE / 2) + (((c & 7) ^ (r & 7)) << 4));
@@ -933,15 +967,15 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         // their exponentials (128 scores in registers spill, and that costs more)
         uint32_t x[2][32];
         float top = -INFINITY;
-#pragma unroll
+#pragma unroll (FP8 && TWO ? 1 : 2)   // (rolled: 4 chunks of 1600 tokens over E4M3 583 against 595 us, over bf16 477 against 472)
         for (int half = 1; half >= 0; --half) {
           tmem_ld32_async(ts + 64 * half, x[0]);
           tmem_ld32_async(ts + 64 * half + 32, x[1]);
           tmem_ld_wait_dep(x[0]);
           tmem_ld_wait_dep(x[1]);
           if (masked) {
-            row_mask(w[2 * half], x[0]);
-            row_mask(w[2 * half + 1], x[1]);
+            row_mask(half ? w[2] : w[0], x[0]);
+            row_mask(half ? w[3] : w[1], x[1]);
           }
           top = max3(top, row_max(x[0]), row_max(x[1]));
         }
@@ -994,101 +1028,43 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
       const bool whole = j0 == 0 && j1 == np;
       const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (j0 == 0 ? 1 : 0);
       constexpr int ROWS = TWO ? 256 : 128;
-      if (seq == 0 && tid == 0) p.cont[blockIdx.x] = j0 > 0;
-      if (j0 == 0 && j1 < np && tid == 0) {
-        RowsSplit d{};
-        d.b = it.b;
-        d.h = it.h;
-        d.tok0 = it.tok0;
-        d.n = it.n;
-        d.row0 = it.row0;
-        d.c_last = static_cast<int>(cta_of_unit(it.first + static_cast<int64_t>(np - 1) * kPage, W, P));
-        if constexpr (LANES) d.c_last = d.c_last * stride + static_cast<int>(blockIdx.x) % stride;
-        d.stride = stride;
-        p.splits[blockIdx.x] = d;
-        split = true;
-      }
-      // Rows leave through shared memory, SEG bytes of each at a time, so that
-      // a store instruction writes whole sectors (8 segments of 64 bytes, or 16
-      // of 32, instead of 32 of 16): this lane writes 16 bytes of rows
-      // i 32 / CH + lane / CH of its warp.  (This code runs once per piece: it
-      // is kept short, its instructions come from far away.)
-      constexpr int SEG = rows_segment(FP8), CH = SEG / 16;
-      uint8_t* stage = smem + p.off_stage + warp * 32 * SEG;
+      // Each thread writes its own row, a sector (32 bytes) a store; 16 columns are
+      // read while those before leave.  (This code runs once per piece: it is kept
+      // short, its instructions come from far away.)
       const bool f32 = !whole || p.out_f32;
-      uint8_t* orow[CH];                     // start of the row (whole: in out, else in this piece's ws_o) + this lane's chunk; null: dead
-#pragma unroll
-      for (int i = 0; i < CH; ++i) {
-        const int rr = 32 * (warp & 3) + i * (32 / CH) + lane / CH;
-        const ushort2 tg = rowmap[rr];
-        const int tk = it.tok0 + (TWO ? s * p.tile_toks : 0) + tg.x;
-        const int64_t row = whole ? static_cast<int64_t>(it.row0 + tk) * g.num_q_heads + it.h * g.group + tg.y
-                                  : slot * ROWS + (TWO ? s * 128 : 0) + rr;
-        orow[i] = tg.x >= p.tile_toks || tk >= it.n
-                      ? nullptr
-                      : (whole ? static_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(p.ws_o)) + row * (D * (f32 ? 4 : 2)) +
-                            16 * (lane % CH);
-      }
+      const bool wide = !whole || (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+      uint8_t* const orow =
+          whole ? static_cast<uint8_t*>(p.out) +
+                      (static_cast<int64_t>(it.row0 + tok) * g.num_q_heads + it.h * g.group + (r - t * g.group)) * (D * (f32 ? 4 : 2))
+                : reinterpret_cast<uint8_t*>(p.ws_o + (slot * ROWS + (TWO ? s * 128 : 0) + r) * D);
       __syncwarp();
       if (lane == 0) mbar_arrive(&iempty[seq % kRowsPieces]);
-      const auto swz = [](int row) -> int { return CH == 4 ? (row >> 1) & 3 : (row >> 2) & 1; };
-      // this row's next SEG bytes in, the warp's rows' out, `off` bytes into the row
-      auto pass = [&](int off, const uint4 (&w)[CH]) {
-#pragma unroll
-        for (int k = 0; k < CH; ++k) *reinterpret_cast<uint4*>(stage + lane * SEG + ((k ^ swz(lane)) << 4)) = w[k];
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-          const int rr = i * (32 / CH) + lane / CH;
-          const uint4 x = *reinterpret_cast<const uint4*>(stage + rr * SEG + (((lane % CH) ^ swz(rr)) << 4));
-          if (orow[i] != nullptr) *reinterpret_cast<uint4*>(orow[i] + off) = x;
-        }
-        __syncwarp();
-      };
-      // columns [c0, c1) of this row: fetch(c, u) starts reading 16 columns into
-      // buffer u, take(c, u, v) gives them; the next block's read runs under a
-      // pass (E4M3: read when taken, its registers are fewer: 151 against 160 us)
+      // columns [c0, c1) of this row: fetch(c) starts reading 16 columns, take(v) gives them
       auto store = [&](int c0, int c1, const auto& fetch, const auto& take) {
-        if (f32) {
-          fetch(c0, 0);
+        fetch(c0);
 #pragma unroll 1
-          for (int c = c0; c < c1; c += 16) {
-            float v[16];
-            take(c, 0, v);
-            if (c + 16 < c1) fetch(c + 16, 0);
+        for (int c = c0; c < c1; c += 16) {
+          float v[16];
+          take(v);
+          if (c + 16 < c1) fetch(c + 16);
+          if (!live) continue;
+          if (f32) {
 #pragma unroll
-            for (int k = 0; k < 4; k += CH) {
-              uint4 w[CH];
+            for (int h = 0; h < 16; h += 8) {
+              uint32_t w[8];
 #pragma unroll
-              for (int u = 0; u < CH; ++u)
-                w[u] = make_uint4(__float_as_uint(v[4 * (k + u)]), __float_as_uint(v[4 * (k + u) + 1]),
-                                  __float_as_uint(v[4 * (k + u) + 2]), __float_as_uint(v[4 * (k + u) + 3]));
-              pass(c * 4 + k * 16, w);
+              for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(v[h + k]);
+              store_sector(orow + c * 4 + h * 4, wide, w);
             }
-          }
-        } else {
+          } else {
+            uint32_t w[8];
 #pragma unroll
-          for (int u = 0; u < CH / 2; ++u) fetch(c0 + 16 * u, u);
-#pragma unroll 1
-          for (int c = c0; c < c1; c += 8 * CH) {
-            uint4 w[CH];
-#pragma unroll
-            for (int u = 0; u < CH / 2; ++u) {
-              float v[16];
-              take(c + 16 * u, u, v);
-              w[2 * u] = make_uint4(pack2<false>(v[0], v[1]), pack2<false>(v[2], v[3]), pack2<false>(v[4], v[5]), pack2<false>(v[6], v[7]));
-              w[2 * u + 1] = make_uint4(pack2<false>(v[8], v[9]), pack2<false>(v[10], v[11]), pack2<false>(v[12], v[13]),
-                                        pack2<false>(v[14], v[15]));
-            }
-            if (c + 8 * CH < c1) {
-#pragma unroll
-              for (int u = 0; u < CH / 2; ++u) fetch(c + 8 * CH + 16 * u, u);
-            }
-            pass(c * 2, w);
+            for (int k = 0; k < 8; ++k) w[k] = pack2<false>(v[2 * k], v[2 * k + 1]);
+            store_sector(orow + c * 2, wide, w);
           }
         }
       };
-      uint32_t o[2][16];
+      uint32_t o[16];
       if constexpr (TWO) {
         if (je > j0) {
           wait_all(&odone[s], (oph >> s) & 1u);
@@ -1099,14 +1075,11 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         const bool none = l == 0.f;   // O may be anything
         store(
             0, D,
-            [&](int c, int u) {
-              if constexpr (!FP8) tmem_ld_async(tl + TM_O + s * 128 + c, o[u]);
-            },
-            [&](int c, int u, float (&v)[16]) {
-              if constexpr (FP8) tmem_ld_async(tl + TM_O + s * 128 + c, o[u]);
-              tmem_ld_wait_dep(o[u]);
+            [&](int c) { tmem_ld_async(tl + TM_O + s * 128 + c, o); },
+            [&](float (&v)[16]) {
+              tmem_ld_wait_dep(o);
 #pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] = none ? 0.f : __uint_as_float(o[u][k]) * f;
+              for (int k = 0; k < 16; ++k) v[k] = none ? 0.f : __uint_as_float(o[k]) * f;
             });
         if (!whole && live) p.ws_lse[slot * ROWS + s * 128 + r] = l == 0.f ? -INFINITY : __log2f(l) - negm;
       } else {
@@ -1125,25 +1098,19 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         const float lt = wa * a.y + wb * b.y;
         const float f = lt == 0.f ? 0.f : (whole ? p.v_scale : 1.f) / lt;
         const float fa = wa * f, fb = wb * f;   // zero where a group had no weight: its O may be anything
-        uint32_t q[2][16];
+        uint32_t q[16];
         store(
             s * (D / 2), (s + 1) * (D / 2),
-            [&](int c, int u) {
-              if constexpr (!FP8) {
-                tmem_ld_async(tl + TM_O + c, o[u]);
-                tmem_ld_async(tl + TM_O + 128 + c, q[u]);
-              }
+            [&](int c) {
+              tmem_ld_async(tl + TM_O + c, o);
+              tmem_ld_async(tl + TM_O + 128 + c, q);
             },
-            [&](int c, int u, float (&v)[16]) {
-              if constexpr (FP8) {
-                tmem_ld_async(tl + TM_O + c, o[u]);
-                tmem_ld_async(tl + TM_O + 128 + c, q[u]);
-              }
-              tmem_ld_wait_dep(o[u]);
-              tmem_ld_wait_dep(q[u]);
+            [&](float (&v)[16]) {
+              tmem_ld_wait_dep(o);
+              tmem_ld_wait_dep(q);
 #pragma unroll
               for (int k = 0; k < 16; ++k)
-                v[k] = (fa == 0.f ? 0.f : __uint_as_float(o[u][k]) * fa) + (fb == 0.f ? 0.f : __uint_as_float(q[u][k]) * fb);
+                v[k] = (fa == 0.f ? 0.f : __uint_as_float(o[k]) * fa) + (fb == 0.f ? 0.f : __uint_as_float(q[k]) * fb);
             });
         if (!whole && s == 0 && live) p.ws_lse[slot * ROWS + r] = lt == 0.f ? -INFINITY : top + __log2f(lt);
         tc_fence_before();
@@ -1151,8 +1118,6 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
       }
       tc_fence_before();
     }
-    if (tid == 0 && !split) p.splits[blockIdx.x].b = -1;
-    if (tid == 0 && seq == 0) p.cont[blockIdx.x] = 0;   // no page starts in its units
   }
 
   for (int b = blockIdx.x; b < g.batch; b += gridDim.x) {  // requests with a bad length: zero rows

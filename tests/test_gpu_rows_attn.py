@@ -491,3 +491,39 @@ def test_a_step_without_tokens():
     T.trtv_verify_tree(p.geom, q, p.pool, p.table, p.kv_lens, empty, mask, torch.empty_like(q), T.TRTV_BF16, ws, nb)
     torch.cuda.synchronize()
     assert T.trtv_get_device_error() == 0
+
+
+@pytest.mark.parametrize("out_dtype", [T.TRTV_BF16, T.TRTV_F32])
+@pytest.mark.parametrize("hq,hk,d,fp8", [(32, 4, 128, False), (8, 2, 64, False), (32, 4, 128, True)])
+def test_buffers_at_the_smallest_alignment(out_dtype, hq, hk, d, fp8):
+    """q, out and the pool 16 bytes past a 32-byte boundary, in prompts and trees of one tile and of two."""
+    def off(x):
+        n = 16 // x.element_size()
+        y = torch.empty(x.numel() + n, dtype=x.dtype, device=x.device)
+        y[n:] = x.flatten()
+        return y[n:].view(x.shape)
+
+    for new in ([130, 3, 40], [7, 9, 2]):
+        p = Rows(new, [70, 500, 0], hq, hk, d, fp8=fp8, pad=2, seed=12)
+        p.q, p.pool = off(p.q), off(p.pool)
+        assert p.q.data_ptr() % 32 == 16
+        ws, nb = p.workspace()
+        out = off(torch.full((p.rows, hq, d), 7.0, device=p.dev,
+                             dtype=torch.float32 if out_dtype == T.TRTV_F32 else torch.bfloat16))
+        T.trtv_prompt_attn(p.geom, p.q, p.pool, p.table, p.kv_lens, p.indptr, out, out_dtype, ws, nb)
+        check(p, out)
+        if p.qo_len <= 128:
+            m = p.tree_masks()
+            out.fill_(7.0)
+            T.trtv_verify_tree(p.geom, p.q, p.pool, p.table, p.kv_lens, p.indptr, pack(m, p.qo_len), out, out_dtype, ws, nb)
+            check(p, out, m)
+
+
+def test_one_request_over_many_ctas():
+    """Small work is cut alike for every KV head, whatever the heads and CTAs."""
+    for hq, hk, num_ctas in ((6, 3, 0), (14, 7, 0), (10, 5, 16), (12, 12, 7), (32, 4, 151)):
+        p = Rows([5], [1900], hq, hk, 128, seed=hq, num_ctas=num_ctas)
+        m = p.tree_masks()
+        check(p, p.tree(m), m)
+        p = Rows([60, 2], [900, 300], hq, hk, 64, seed=hq, num_ctas=num_ctas)
+        check(p, p.prompt())

@@ -188,7 +188,7 @@ __device__ __forceinline__ int64_t rows_units(const RowsAttnParams& p, int b, in
 // the same time, so that one read of HBM serves them.
 template <bool LANES>
 __device__ __forceinline__ bool rows_scan(const RowsAttnParams& p, int toks, bool causal, int items, int64_t* scan,
-                                          int64_t* warp_tot) {
+                                          int64_t* warp_tot, int& requests) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nthr = blockDim.x, n = p.g.batch, warps = nthr / 32;
   const int seg = (n + nthr - 1) / nthr, lo = min(n, tid * seg), hi = min(n, lo + seg);
   int64_t all = 0, one = 0;
@@ -214,7 +214,7 @@ __device__ __forceinline__ bool rows_scan(const RowsAttnParams& p, int toks, boo
     }
     if (lane == 31) warp_tot[warps + warp] = incl_one;
   }
-  __syncthreads();
+  requests = __syncthreads_count(all > 0);   // (batches beyond a thread each: fewer)
   bool lanes = false;
   if constexpr (LANES) {
     int64_t w_all = 0, w_one = 0;
@@ -507,16 +507,25 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
     tmem_relinquish();
   }
   pdl_wait();   // inputs may come from the previous kernel of the stream
-  const bool lanes = rows_scan<LANES>(p, toks, causal, LANES ? p.items : 1, scan, scan + g.batch + 1);
+  int requests;
+  const bool lanes = rows_scan<LANES>(p, toks, causal, LANES ? p.items : 1, scan, scan + g.batch + 1, requests);
   pdl_trigger();
   const int64_t W = scan[g.batch];
   // little work is spread over fewer CTAs: pieces of less than kRowsLeast
-  // positions cost more to join than they save
+  // positions cost more to join than they save.  One-tile items of many pages (A
+  // positions a head) are cut less than that: a page takes 0.35 us, four more pieces
+  // 1.75 us of the join, so a piece is best some 10 sqrt(A) long (a tree of 8 over
+  // 8000 positions 28.5 -> 21.2 us, over 30000 36.5 -> 32.0, two over 4-9 k 27.9 ->
+  // 22.9; factors of 8, 12 and 16 21.2 / 21.3 / 23.2, 32.1 / 33.2 / 35.1).
   const int stride = LANES && lanes ? p.items : 1, rank = static_cast<int>(blockIdx.x) / stride;
+  int64_t P = max(int64_t{1}, min(static_cast<int64_t>(p.num_ctas / stride), W / kRowsLeast));
+  if (!TWO && P > 16) {   // (16 pieces or fewer: not worth the arithmetic)
+    const float per_head = static_cast<float>(W) / static_cast<float>(max(requests, 1) * g.num_kv_heads);
+    P = min(P, W / max(kRowsLeast, static_cast<int>(10.f * sqrtf(per_head)) - 64));
+  }
   // (a multiple of the KV heads: one request's heads are then all cut alike, no CTA
   // has the end of one and the start of the next; a tree of 8 over 900 positions
   // 14.0 us, 17.5 on 15 or 18 CTAs)
-  int64_t P = max(int64_t{1}, min(static_cast<int64_t>(p.num_ctas / stride), W / kRowsLeast));
   if (P < p.num_ctas / stride && P > g.num_kv_heads) P -= static_cast<int>(P) % g.num_kv_heads;
   const int64_t u0 = rows_begin(rank, W, P), u1 = rows_begin(rank + 1, W, P);
   tc_fence_before();

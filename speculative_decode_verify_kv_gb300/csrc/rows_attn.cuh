@@ -502,11 +502,13 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
     *abortf = 0;
     fence_mbar_init();
   }
+  pdl_wait();   // inputs may come from the previous kernel of the stream
+  // (TMEM only now: a CTA that held it while it waits for the previous kernel could
+  // keep it from a CTA of that kernel on the same SM)
   if (warp == 9) {
     tmem_alloc(tslot, 512);
     tmem_relinquish();
   }
-  pdl_wait();   // inputs may come from the previous kernel of the stream
   int requests;
   const bool lanes = rows_scan<LANES>(p, toks, causal, LANES ? p.items : 1, scan, scan + g.batch + 1, requests);
   pdl_trigger();

@@ -372,8 +372,9 @@ trtv_status trtv_draft_attn_p32(const trtv_geom* geom, const void* q, const void
  * sm_scale * k_scale >= 2^-64.
  * A request whose qo_indptr entries are not ascending within
  * [0, num_tokens], or give more than qo_len tokens, is left out
- * (TRTV_DEVERR_INDPTR); one with kv_len < n_b or beyond 128 * max_pages_per_req
- * sets TRTV_DEVERR_KV_LEN.
+ * (TRTV_DEVERR_INDPTR) and the others are not; a row that a table out of order
+ * gives to two of those may get either's results.  A request with kv_len < n_b or
+ * beyond 128 * max_pages_per_req sets TRTV_DEVERR_KV_LEN.
  */
 
 /* Inputs of trtv_norm_rope_stage (device pointers; strides in elements). */
@@ -475,7 +476,8 @@ trtv_status trtv_verify_tree(const trtv_geom* geom, const void* q, const void* k
  * Rows at or past the new length keep what they held.  A request with a bad
  * path (TRTV_DEVERR_PATH), kv_len or qo_indptr entry, or whose tree touches a
  * page that names no slot (TRTV_DEVERR_PAGE_ID), is not moved and keeps its
- * length, as does one without tokens.  qo_len <= 128.
+ * length, as does one without tokens.  qo_len <= 128.  (No rows are read here:
+ * qo_indptr's entries are held against each other and qo_len, not num_tokens.)
  */
 trtv_status trtv_tree_commit(const trtv_geom* geom, void* kv_pool, const int32_t* page_table,
                              const int32_t* kv_lens, const int32_t* qo_indptr,

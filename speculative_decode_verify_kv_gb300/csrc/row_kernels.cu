@@ -87,10 +87,9 @@ __global__ void __launch_bounds__(kStageThreads) norm_rope_stage_kernel(const __
   Rows cur;
   load(h0, cur);   // before the token's request is known
 
-  const int b = row_request(g, tok, lane);
-  if (b >= g.batch) return;   // equal rows per request, and more of them than requests
-  const RowSpan span = row_span(g, b);
-  if (!span.ok || tok < span.row0 || tok >= span.row0 + span.n) return;  // nobody's row
+  RowSpan span;
+  const int b = row_owner(g, tok, lane, span);
+  if (b >= g.batch) return;   // nobody's row
   const int L = g.kv_lens[b];
   const bool len_ok = len_valid(L, span.n, g.max_pages);
   const int cell = L - span.n + (tok - span.row0);   // >= 0 and below the capacity when len_ok

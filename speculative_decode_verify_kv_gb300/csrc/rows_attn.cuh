@@ -19,10 +19,10 @@
 // rows_scan; 16 trees of 512 rows over 16-32 k positions: 6 % faster).
 //
 // Per page and tile: S = Q K^T (128 x 128, fp32 in TMEM), softmax in registers
-// (running maximum, moved only when it rises by more than 2^8; sums in fp32 of
-// the unrounded weights), P back over S as 16-bit pairs -- 8 (bf16) or 11 (f16)
-// significant bits, the rounding of the second product's operand -- and
-// O += P V (fp32 in TMEM).  The issuing warp orders QK of the next page behind
+// (running maximum, moved only when it rises by more than 2^8, E4M3 caches 2^4;
+// sums in fp32 of the unrounded weights), P back over S as 16-bit pairs -- 8
+// (bf16) or 11 (f16) significant bits, the rounding of the second product's
+// operand -- and O += P V (fp32 in TMEM).  The issuing warp orders QK of the next page behind
 // PV of this one, tile by tile, so one group's softmax runs under the other's
 // products; UMMAs complete in order, so S may be overwritten by a QK issued
 // after the PV that reads P there, and S ready means the PV before it is done.
@@ -30,7 +30,11 @@
 // E4M3 caches: four warps turn each page's codes into f16 (exact) in the UMMA's
 // layout, and each row of Q is scaled by a power of two into f16's range
 // (exact for elements within 2^-29 of the row's largest), undone in the logits'
-// scale.
+// scale.  f16 has few exponents, so P is lifted by 2^10: the weight of the
+// reference maximum is 2^10, a row may outgrow it to 2^14, and down to 2^-24 of it
+// a weight keeps its 11 bits.  Below, it is off by at most 2^-35 of it (under the
+// other weights' rounding for fewer than 2^24 positions; without the lift, weights
+// under 2^-25 were lost: 0.4 % of the sum in a row of one large and 131072 small).
 //
 // What bounds a prompt's page is one group's chain: softmax, then PV and the
 // next QK, which cannot start before P is written over S.  So a row's scores are
@@ -52,6 +56,7 @@ namespace trtv {
 constexpr int kConvertWarps = 4;   // warps that convert a tile of E4M3 codes, all of them every tile
 constexpr int kRowsLeast = 256;
 constexpr float kRowsLazy = 8.0f;   // log2 of how far a row may outgrow its reference maximum
+constexpr float kRowsLazyF16 = 4.0f, kRowsLiftF16 = 10.0f;   // E4M3 caches: the same, and log2 of that maximum's weight
 
 // ---- items ------------------------------------------------------------------
 
@@ -394,6 +399,14 @@ __device__ __forceinline__ float row_max(const uint32_t (&x)[32]) {
   return fmaxf(a, b);
 }
 
+// A pair of weights as f16; past its range (the scores' own rounding can leave a
+// row that far above its maximum where they pass 2^23) its largest value.
+__device__ __forceinline__ uint32_t pack2_f16_sat(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // Weights 2^(x scale + negm) of columns 32 c .. 32 c + 31, stored over the scores
 // as 16-bit pairs (column ts + i of P holds positions 2i and 2i + 1); their sum
 // is added to `sum`.
@@ -411,7 +424,7 @@ __device__ __forceinline__ void row_exp(uint32_t ts, int c, const uint32_t (&x)[
       v.x = fast_exp2(v.x);
       v.y = fast_exp2(v.y);
       sum = __fadd2_rn(sum, v);
-      o[k] = pack2<F16>(v.x, v.y);
+      o[k] = F16 ? pack2_f16_sat(v.x, v.y) : pack2<false>(v.x, v.y);
     }
     if constexpr (F16) tmem_st8(ts + 16 * c + h, o);
     else tmem_st16(ts + 16 * c, o);
@@ -948,11 +961,12 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           if (lane == 0) mbar_arrive(&qconv[slot]);
         }
       }
-      const float lazy = kRowsLazy / scale;
+      constexpr float LIFT = FP8 ? kRowsLiftF16 : 0.f;
+      const float lazy = (FP8 ? kRowsLazyF16 : kRowsLazy) / scale;
       const int bound = live ? ctx + tok : -1;      // causal: its last position
       // first position that some row of the tile does not see
       const int open = causal ? ctx + it.tok0 + (TWO ? s * p.tile_toks : 0) + 1 : ctx;
-      float m = -INFINITY, negm = 0.f, l = 0.f;     // reference maximum (raw), -m scale, sum
+      float m = -INFINITY, negm = LIFT, l = 0.f;    // reference maximum (raw), -m scale + LIFT, sum
       for (int j = TWO ? it.j0 : it.j0 + s; j < je; j += TWO ? 1 : 2) {
         wait_all(&sfull[s], sph);
         sph ^= 1u;
@@ -994,7 +1008,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           const bool first = m == -INFINITY;
           const bool grow = top > m + lazy;
           if (grow) m = top;
-          const float nn = m == -INFINITY ? 0.f : -m * scale;
+          const float nn = (m == -INFINITY ? 0.f : -m * scale) + LIFT;
           if (__any_sync(0xffffffffu, grow && !first)) {
             // S ready: the PV before it has retired, O is stable
             const float alpha = grow && !first ? fast_exp2(nn - negm) : 1.f;   // 2^((old m - new m) scale)

@@ -406,7 +406,8 @@ typedef struct {
  * All in binary32 with one rounding at the end: q_out gets bf16; the cache row
  * of the token's position (as trtv_stage_kv) gets the key as bf16, or as
  * E4M3(y / k_scale), and the value's bits, or E4M3(v / v_scale) (binary32
- * quotient, round to nearest even, saturated to +-448, NaN kept).
+ * quotient, round to nearest even, saturated to +-448, NaN kept; a v_scale of
+ * zero is refused).
  *   q_out      bf16 [num_tokens, num_q_heads, head_dim] (written), may be q
  *              itself when q_stride = num_q_heads * head_dim
  * All pointers 16-byte aligned, but page_table, kv_lens, qo_indptr and

@@ -243,6 +243,7 @@ trtv_status trtv_norm_rope_stage(const trtv_geom* g, const trtv_norm_rope* in, c
     return TRTV_ERR_INVALID_ARG;
   if (in->rot_dim > 0 && (in->rope_table == nullptr || in->table_len < 1)) return TRTV_ERR_INVALID_ARG;
   if (in->q == q_out && in->q_stride != qw) return TRTV_ERR_INVALID_ARG;
+  if (g->kv_dtype == TRTV_FP8_E4M3 && g->v_scale == 0.f) return TRTV_ERR_INVALID_ARG;   // values are divided by it
   const void* ptrs[] = {in->q, in->k, in->v, in->q_weight, in->k_weight, in->rope_table, q_out, kv_pool};
   for (const void* x : ptrs)
     if (!aligned(x, 16)) return TRTV_ERR_INVALID_ARG;

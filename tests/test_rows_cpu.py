@@ -131,3 +131,11 @@ def test_no_rows_no_buffers(lib):
     assert lib.trtv_verify_tree(r, None, None, None, None, 16, 0, None, None, 0, None, 0, None) == 0
     assert lib.trtv_prompt_attn(r, None, None, None, None, 16, 0, None, 0, None, 0, None) == 0
     assert lib.trtv_verify_tree(r, 16, 16, 16, 16, 16, -1, None, 16, 0, 256, 1 << 40, None) == INVALID
+
+
+@pytest.mark.parametrize("v_scale", [0.0, -0.0])
+def test_stage_divides_by_no_zero(lib, v_scale):
+    """Staging into an E4M3 cache divides the values by v_scale."""
+    n = T.NormRope(q=32, k=16, v=16, q_stride=4096, k_stride=4096, v_stride=4096)
+    r = ctypes.byref(geom(kv_dtype=1, v_scale=v_scale))
+    assert lib.trtv_norm_rope_stage(r, ctypes.byref(n), 16, 80, 16, 16, 16, 16, None) == INVALID

@@ -403,11 +403,11 @@ typedef struct {
  *   y = x * (mean(x^2) + eps)^(-1/2) * q_weight (k_weight), then for i <
  *   rot_dim / 2 with (c, s) = (rope_table[pos][i], rope_table[pos][rot_dim / 2 + i])
  *   (y1, y2) -> (y1 c - y2 s, y2 c + y1 s), (y1, y2) the i-th pair.
- * All in binary32 with one rounding at the end: q_out gets bf16; the cache row
- * of the token's position (as trtv_stage_kv) gets the key as bf16, or as
- * E4M3(y / k_scale), and the value's bits, or E4M3(v / v_scale) (binary32
- * quotient, round to nearest even, saturated to +-448, NaN kept; a v_scale of
- * zero is refused).
+ * All in binary32 (a head whose squares pass its range comes out as zeros) with
+ * one rounding at the end: q_out gets bf16; the cache row of the token's position
+ * (as trtv_stage_kv) gets the key as bf16, or as E4M3(y / k_scale), and the
+ * value's bits, or E4M3(v / v_scale) (binary32 quotient, round to nearest even,
+ * saturated to +-448, NaN kept; a v_scale of zero is refused).
  *   q_out      bf16 [num_tokens, num_q_heads, head_dim] (written), may be q
  *              itself when q_stride = num_q_heads * head_dim
  * All pointers 16-byte aligned, but page_table, kv_lens, qo_indptr and

@@ -307,7 +307,7 @@ def trtv_get_device_error(stream=None) -> int:
 _torch = None
 
 
-def _begin(fn: str, stream):
+def _begin(stream):
     """(current device, raw stream) of a call."""
     global _torch
     if _torch is None:
@@ -373,7 +373,7 @@ def trtv_norm_rope_stage(geom: Geom, q, k, v, q_weight, k_weight, eps: float, ro
     """Per-head norm of queries and keys, rotation, and K/V staging of packed token rows: q [rows, Hq, D],
     k, v [rows, Hk, D] bf16, each possibly a view of one projection; q_out [rows, Hq, D] bf16."""
     fn = "trtv_norm_rope_stage"
-    dev, st = _begin(fn, stream)
+    dev, st = _begin(stream)
     bf16, d = _torch.bfloat16, geom.head_dim
     rows = q.shape[0]
     qs, ks = (rows, geom.num_q_heads, d), (rows, geom.num_kv_heads, d)
@@ -399,7 +399,7 @@ def trtv_workspace_bytes_rows(geom: Geom) -> int:
 
 def _rows_attn(fn: str, geom: Geom, q, kv_pool, page_table, kv_lens, qo_indptr, tree_mask, out, out_dtype: int,
                workspace, ws_bytes: int, stream) -> None:
-    dev, st = _begin(fn, stream)
+    dev, st = _begin(stream)
     rows = q.shape[0]
     shape = (rows, geom.num_q_heads, geom.head_dim)
     pt, kl, ip = _tables(fn, geom, page_table, kv_lens, qo_indptr, dev)
@@ -436,7 +436,7 @@ def trtv_tree_commit(geom: Geom, kv_pool, page_table, kv_lens, qo_indptr, path, 
                      stream=None) -> None:
     """Accepted path's cache rows to the front of the tree's positions, and the new lengths."""
     fn = "trtv_tree_commit"
-    dev, st = _begin(fn, stream)
+    dev, st = _begin(stream)
     i32, b = _torch.int32, geom.batch
     pt, kl, ip = _tables(fn, geom, page_table, kv_lens, qo_indptr, dev)
     width = path.shape[1]

@@ -19,10 +19,10 @@
 // rows_scan; 16 trees of 512 rows over 16-32 k positions: 6 % faster).
 //
 // Per page and tile: S = Q K^T (128 x 128, fp32 in TMEM), softmax in registers
-// (running maximum, moved only when it rises by more than 2^8, E4M3 caches 2^4;
-// sums in fp32 of the unrounded weights), P back over S as 16-bit pairs -- 8
-// (bf16) or 11 (f16) significant bits, the rounding of the second product's
-// operand -- and O += P V (fp32 in TMEM).  The issuing warp orders QK of the next page behind
+// (running maximum, moved only when it rises by more than 2^8; sums in fp32 of
+// the unrounded weights), P back over S as 16-bit pairs -- 8 (bf16) or 11 (f16)
+// significant bits, the rounding of the second product's operand -- and
+// O += P V (fp32 in TMEM).  The issuing warp orders QK of the next page behind
 // PV of this one, tile by tile, so one group's softmax runs under the other's
 // products; UMMAs complete in order, so S may be overwritten by a QK issued
 // after the PV that reads P there, and S ready means the PV before it is done.
@@ -30,11 +30,13 @@
 // E4M3 caches: four warps turn each page's codes into f16 (exact) in the UMMA's
 // layout, and each row of Q is scaled by a power of two into f16's range
 // (exact for elements within 2^-29 of the row's largest), undone in the logits'
-// scale.  f16 has few exponents, so P is lifted by 2^10: the weight of the
-// reference maximum is 2^10, a row may outgrow it to 2^14, and down to 2^-24 of it
-// a weight keeps its 11 bits.  Below, it is off by at most 2^-35 of it (under the
-// other weights' rounding for fewer than 2^24 positions; without the lift, weights
-// under 2^-25 were lost: 0.4 % of the sum in a row of one large and 131072 small).
+// scale.  f16 has few exponents, so P is lifted by 2^7: the reference maximum's
+// weight is 2^7, a row may outgrow it to 2^15, and down to 2^-21 of it a weight
+// keeps its 11 bits.  Below, it is off by at most 2^-32 of it, less than the other
+// weights' rounding in a piece of up to 2^21 positions (not lifted, weights under
+// 2^-25 were lost: 0.4 % of the sum in a row of one large and 131072 small).  A
+// reference that moves at 2^4, with a lift of 2^10, takes 2242 us where logits have a
+// deviation of 6 (a prompt of 16384), 2206 so.
 //
 // What bounds a prompt's page is one group's chain: softmax, then PV and the
 // next QK, which cannot start before P is written over S.  So a row's scores are
@@ -56,7 +58,7 @@ namespace trtv {
 constexpr int kConvertWarps = 4;   // warps that convert a tile of E4M3 codes, all of them every tile
 constexpr int kRowsLeast = 256;
 constexpr float kRowsLazy = 8.0f;   // log2 of how far a row may outgrow its reference maximum
-constexpr float kRowsLazyF16 = 4.0f, kRowsLiftF16 = 10.0f;   // E4M3 caches: the same, and log2 of that maximum's weight
+constexpr float kRowsLiftF16 = 7.0f;   // E4M3 caches: log2 of that maximum's weight
 
 // ---- items ------------------------------------------------------------------
 
@@ -400,7 +402,7 @@ __device__ __forceinline__ float row_max(const uint32_t (&x)[32]) {
 }
 
 // A pair of weights as f16; past its range (the scores' own rounding can leave a
-// row that far above its maximum where they pass 2^23) its largest value.
+// row that far above its maximum where they pass 2^22) its largest value.
 __device__ __forceinline__ uint32_t pack2_f16_sat(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -962,7 +964,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         }
       }
       constexpr float LIFT = FP8 ? kRowsLiftF16 : 0.f;
-      const float lazy = (FP8 ? kRowsLazyF16 : kRowsLazy) / scale;
+      const float lazy = kRowsLazy / scale;
       const int bound = live ? ctx + tok : -1;      // causal: its last position
       // first position that some row of the tile does not see
       const int open = causal ? ctx + it.tok0 + (TWO ? s * p.tile_toks : 0) + 1 : ctx;

@@ -1,7 +1,7 @@
 """How exactly prompt and tree attention weigh positions that count for little.
 
 E4M3 caches take the weights into the second product as f16 (2^-11 of a weight;
-below 2^-24 of the row's reference maximum 2^-35 of that), bf16 caches as bf16
+below 2^-21 of the row's reference maximum 2^-32 of that), bf16 caches as bf16
 (2^-8 of a weight).  Besides that, with N positions: the product is summed in
 N / 16 steps that may each cut off a unit in the last place of its result
 (2^-23), the weights in binary32 (N / 128 roundings of 2^-24 and some within a
@@ -53,7 +53,7 @@ def line(n, fp8, unit, codes, values, hq=1, qo_len=1, num_ctas=1):
 
 def tail_tolerance(n, fp8, bits, mag):
     """See the head of this file; `bits`: the logits' span."""
-    return ((2.0 ** -11 + n * 2.0 ** -35 if fp8 else 2.0 ** -8) + n / 16 * 2.0 ** -23 + n / 128 * 2.0 ** -24 + 64 * 2.0 ** -24 +
+    return ((2.0 ** -11 + n * 2.0 ** -32 if fp8 else 2.0 ** -8) + n / 16 * 2.0 ** -23 + n / 128 * 2.0 ** -24 + 64 * 2.0 ** -24 +
             2 * bits * 2.0 ** -24) * mag + 1e-7
 
 

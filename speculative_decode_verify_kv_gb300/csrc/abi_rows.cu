@@ -16,13 +16,16 @@ constexpr int kMaxBatch = 2048;   // the requests' scan lies in shared memory
 constexpr int kMaxTreeTokens = 128;
 constexpr int kMaxHeads = 65536;  // a token's row is indexed by 32 bits
 constexpr float kMinScale = 5.421011e-20f;  // 2^-64
-// stream-K charge of an item in positions, what switching items costs.  256-row
-// items, bf16: 8 prompts of up to 4000 tokens 459 / 435 / 439 / 450 / 455 us at
-// 192 / 256 / 320 / 384 / 512; E4M3: a prompt of 16384 1674 / 1626 / 1635 / 1647 at
-// 384 / 448 / 512 / 640, 4 chunks over 2-12 k positions 148.0 / 147.5 / 146.7 /
-// 146.5.  One tile: 64 trees of 16 nodes 108.2 / 106.7 / 105.7 / 104.4 at 64 / 96 /
-// 128 / 256, but one tree of 8 over 900 positions is cut best at 128; over E4M3 112.9
-// / 111.5 / 110.5 / 105.8.
+// stream-K charge of an item in positions, what switching items costs (us).
+// 256-row items, at 128 / 256 / 384 / 512: 8 prompts of up to 4000 tokens 501 / 460 /
+// 461 / 471, of head_dim 64 394 / 373 / 382 / 391, one of 16384 of head_dim 64 1167 /
+// 1142 / 1148 / 1155.  E4M3, at 256 / 384 / 512 / 640: 8 prompts 699 / 624 / 601 / 612,
+// one of 16384 1783 / 1671 / 1625 / 1633, 4 chunks over 2-12 k positions 146.4 / 143.7 /
+// 142.1 / 142.5.  One tile, at 64 / 128 / 256: 64 trees of 16 nodes 113.2 / 110.5 /
+// 109.8 (head_dim 64 74.6 / 73.0 / 69.6), but little work is cut best at 128: one tree
+// of 8 over 900 positions 14.0 / 13.4 / 15.0 (head_dim 64 12.1 / 11.1 / 12.5), three over
+// 700-1500 17.0 / 15.6 / 16.1.  E4M3, at 64 / 128 / 256 / 384: 64 trees 113.1 / 110.8 /
+// 105.8 / 100.7, one over 700 14.4 / 14.5 / 15.0 / 14.4, one over 16000 30.0 at each.
 constexpr int kRowsSetupTwo = 256, kRowsSetupTwoFp8 = 512, kRowsSetupOne = 128, kRowsSetupOneFp8 = 256;
 
 // Geometry checks shared by the packed-row calls.

@@ -24,9 +24,11 @@ namespace trtv {
 // Bound by the bytes: 12 prompts, 72 heads of 128, 1.07 GB: 176 us = 6.1 TB/s,
 // 90 % of the copy rate (8 heads a warp and no look-ahead: 294 us; batches of
 // 1 / 3 / 4 rows: 203 / 185 / 195 us; blocks of 256 threads: 189 us).  An E4M3
-// cache and fewer tokens (192 MB, 40 heads): 41.7 us = 68 %, two instruction
-// issues in three taken (pairing chosen at run time: 43.1 us; a branch per kind
-// of head instead of selects: 50 us, the rows' latencies no longer overlap).
+// cache and fewer tokens (9599 of 40 heads, 192 MB): 41.7 us = 68 %.  Seven blocks
+// fit on an SM, 4256 tokens are a round of warps, so these take three rounds, the last
+// a quarter full: 8512 / 8960 / 9600 / 12768 / 25536 tokens take 34.7 / 40.0 / 41.1 /
+// 49.8 / 93.6 us, six full rounds 80 % (pairing chosen at run time: 43.1 us; a branch
+// per kind of head instead of selects: 50 us, the rows' latencies no longer overlap).
 constexpr int kStageThreads = 128;
 constexpr int kStageRows = 2;   // rows in flight per lane group, twice
 

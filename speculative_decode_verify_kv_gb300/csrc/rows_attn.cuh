@@ -16,7 +16,8 @@
 // first position).  Pieces of an item cut between CTAs are joined by
 // rows_join_kernel.  LANES: a tree of more than 256 rows has several items a KV
 // head that read the same pages; the CTAs walk in as many lanes, abreast (see
-// rows_scan; 16 trees of 512 rows over 16-32 k positions: 6 % faster).
+// rows_scan; 16 trees of 512 rows over 16-32 k positions: 5 % faster, over E4M3
+// 0.4 % slower).
 //
 // Per page and tile: S = Q K^T (128 x 128, fp32 in TMEM), softmax in registers
 // (running maximum, moved only when it rises by more than 2^8; sums in fp32 of
@@ -533,7 +534,9 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
   // positions a head) are cut less than that: a page takes 0.35 us, four more pieces
   // 1.75 us of the join, so a piece is best some 10 sqrt(A) long (a tree of 8 over
   // 8000 positions 28.5 -> 21.2 us, over 30000 36.5 -> 32.0, two over 4-9 k 27.9 ->
-  // 22.9; factors of 8, 12 and 16 21.2 / 21.3 / 23.2, 32.1 / 33.2 / 35.1).
+  // 22.9; factors of 8, 12 and 16 21.2 / 21.3 / 23.2, 32.1 / 33.2 / 35.1), 64 off it
+  // (0 / 32 / 64 / 96 / 128 off: one over 3000 17.7 / 17.6 / 17.0 / 16.9 / 17.5, three over
+  // 700-1500 17.5 / 17.2 / 15.7 / 17.9 / 17.9, over 30000 34.5 / 34.3 / 34.1 / 34.3 / 34.1).
   const int stride = LANES && lanes ? p.items : 1, rank = static_cast<int>(blockIdx.x) / stride;
   int64_t P = max(int64_t{1}, min(static_cast<int64_t>(p.num_ctas / stride), W / kRowsLeast));
   if (!TWO && P > 16) {   // (16 pieces or fewer: not worth the arithmetic)

@@ -30,6 +30,14 @@
  *              group (p % 128) / 32, row p % 32 of its head.  The pool holds
  *              num_slots * slot_stride buffers; its address must be 16-byte
  *              aligned.
+ *              E2M1 caches (TRTV_FP4_E2M1, 4.5 bits an element) hold, in place of
+ *              each head's 32 rows of a group, 18 * head_dim bytes: 32 rows of
+ *              head_dim / 2 bytes of E2M1 codes (1 sign, 2 exponent, 1 mantissa
+ *              bit; dim 2i in the low half of byte i, dim 2i + 1 in the high
+ *              half), then 32 rows of head_dim / 16 E4M3 scales, one for each 16
+ *              dims.  A value is code * scale, times k_scale (v_scale).  They are
+ *              read and written by trtv_verify_dense and by the packed-row and
+ *              page calls; the other calls return TRTV_ERR_UNSUPPORTED.
  *   page_table int32 [batch, max_pages_per_req]; entries past a request's
  *              pages are ignored (conventionally 0).
  *   kv_lens    int32 [batch], read on the device at run time (may change
@@ -74,7 +82,7 @@ typedef enum {
   TRTV_ERR_WORKSPACE = 4
 } trtv_status;
 
-typedef enum { TRTV_BF16 = 0, TRTV_FP8_E4M3 = 1, TRTV_F32 = 2 } trtv_dtype;
+typedef enum { TRTV_BF16 = 0, TRTV_FP8_E4M3 = 1, TRTV_F32 = 2, TRTV_FP4_E2M1 = 3 } trtv_dtype;
 
 /* Device error word bits (trtv_get_device_error). */
 #define TRTV_DEVERR_KV_LEN 1    /* kv_len < qo_len or kv_len > 128 * max_pages */
@@ -98,7 +106,7 @@ typedef struct {
   int32_t max_pages_per_req; /* page-table row pitch (capacity / 128) */
   int32_t num_slots;         /* slots in the pool; page ids must be < num_slots */
   int32_t slot_stride;       /* page buffers per slot, >= 2 (V = K + 1: kv_offset == 1) */
-  int32_t kv_dtype;          /* TRTV_BF16 or TRTV_FP8_E4M3 */
+  int32_t kv_dtype;          /* TRTV_BF16, TRTV_FP8_E4M3 or TRTV_FP4_E2M1 */
   float sm_scale;            /* softmax scale, e.g. 1 / sqrt(D) */
   float k_scale;             /* per-tensor dequantisation scale of K (1 for bf16) */
   float v_scale;             /* per-tensor dequantisation scale of V (1 for bf16) */
@@ -134,7 +142,7 @@ trtv_status trtv_subpage_view(const trtv_geom* geom, const int32_t* page_table,
 /*
  * Workspace bytes that trtv_verify_dense and trtv_msa_sparse_attn need for
  * this geometry (topk = the sparse path's k, 0 for dense only); 0 on invalid
- * geometry.  The workspace is caller-allocated device memory, 256-byte
+ * geometry, and with topk for an E2M1 cache.  The workspace is caller-allocated device memory, 256-byte
  * aligned, with no initial contents required: every call writes each byte it
  * reads (split-KV partials, split descriptors, the sparse plan) before reading
  * it.  Calls that may overlap on the GPU must not share a workspace.
@@ -149,6 +157,8 @@ size_t trtv_workspace_bytes(const trtv_geom* geom, int32_t topk);
  * k_p / v_p from KV head hq / G of request b.  Split-KV across CTAs; the
  * split sequences are merged by log-sum-exp in a second kernel launched on the
  * same stream; fp32 accumulation.  out_dtype: TRTV_BF16 or TRTV_F32.
+ * E2M1 caches: trtv_prompt_attn's kernels with qo_len rows per request (its
+ * limits; q, kv_pool and out 16-byte aligned).
  */
 trtv_status trtv_verify_dense(const trtv_geom* geom, const void* q, const void* kv_pool,
                               const int32_t* page_table, const int32_t* kv_lens, void* out,
@@ -407,7 +417,10 @@ typedef struct {
  * one rounding at the end: q_out gets bf16; the cache row of the token's position
  * (as trtv_stage_kv) gets the key as bf16, or as E4M3(y / k_scale), and the
  * value's bits, or E4M3(v / v_scale) (binary32 quotient, round to nearest even,
- * saturated to +-448, NaN kept; a v_scale of zero is refused).
+ * saturated to +-448, NaN kept; a v_scale of zero is refused).  E2M1 caches: of
+ * each 16 dims, t = y / k_scale (v / v_scale), the scale s = E4M3(max |t| / 6) as
+ * above, the codes E2M1(t / s), nearest even and saturated to +-6 (zeros where s
+ * is zero); binary32 quotients; 16 dims with a NaN read as NaN.
  *   q_out      bf16 [num_tokens, num_q_heads, head_dim] (written), may be q
  *              itself when q_stride = num_q_heads * head_dim
  * All pointers 16-byte aligned, but page_table, kv_lens, qo_indptr and
@@ -419,6 +432,19 @@ typedef struct {
 trtv_status trtv_norm_rope_stage(const trtv_geom* geom, const trtv_norm_rope* in, const int32_t* qo_indptr,
                                  int32_t num_tokens, void* q_out, void* kv_pool, const int32_t* page_table,
                                  const int32_t* kv_lens, void* stream);
+
+/*
+ * The cache rows of the packed tokens, read back as bf16: row r, token t of
+ * request b, gets the K and V rows of position c_b + t, as the attention calls
+ * see them (E4M3 and E2M1: code times scales, in binary32, rounded to bf16).
+ *   k_out, v_out  bf16 [num_tokens, num_kv_heads, head_dim], 16-byte aligned
+ *                 (written); either may be NULL
+ * Rows of a request with a bad kv_len, and of a token whose page names no slot
+ * (TRTV_DEVERR_PAGE_ID), are zero.
+ */
+trtv_status trtv_read_kv(const trtv_geom* geom, const void* kv_pool, const int32_t* page_table,
+                         const int32_t* kv_lens, const int32_t* qo_indptr, int32_t num_tokens, void* k_out,
+                         void* v_out, void* stream);
 
 /*
  * Workspace bytes of trtv_prompt_attn and trtv_verify_tree for this geometry;

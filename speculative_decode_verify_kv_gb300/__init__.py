@@ -16,18 +16,18 @@ from typing import Optional
 from . import _build
 
 __all__ = [
-    "TRTV_OK", "TRTV_BF16", "TRTV_FP8_E4M3", "TRTV_F32", "TrtvError", "Geom", "load",
+    "TRTV_OK", "TRTV_BF16", "TRTV_FP8_E4M3", "TRTV_F32", "TRTV_FP4_E2M1", "TrtvError", "Geom", "load",
     "trtv_subpage_view", "trtv_workspace_bytes", "trtv_verify_dense", "trtv_msa_proxy_score",
     "trtv_msa_topk", "trtv_msa_sparse_attn", "trtv_get_device_error", "trtv_version",
     "trtv_verify_dense_noalloc", "trtv_stage_kv", "trtv_flatten_page_table",
     "trtv_page_table_from_flat", "trtv_workspace_bytes_flat", "trtv_verify_dense_flat",
     "trtv_draft_attn_p32", "trtv_msa_select", "trtv_msa_verify", "trtv_status_string",
     "trtv_test_withhold_pages", "trtv_norm_rope_stage", "trtv_workspace_bytes_rows", "trtv_prompt_attn",
-    "trtv_verify_tree", "trtv_tree_commit", "NormRope", "geom_of", "EXPORTS",
+    "trtv_verify_tree", "trtv_tree_commit", "trtv_read_kv", "NormRope", "geom_of", "EXPORTS",
 ]
 
 TRTV_OK, TRTV_ERR_INVALID_ARG, TRTV_ERR_UNSUPPORTED, TRTV_ERR_CUDA, TRTV_ERR_WORKSPACE = range(5)
-TRTV_BF16, TRTV_FP8_E4M3, TRTV_F32 = 0, 1, 2
+TRTV_BF16, TRTV_FP8_E4M3, TRTV_F32, TRTV_FP4_E2M1 = 0, 1, 2, 3
 DEVERR_KV_LEN, DEVERR_PAGE_ID, DEVERR_BLOCK_IDX, DEVERR_TIMEOUT = 1, 2, 4, 8
 DEVERR_INDPTR, DEVERR_POSITION, DEVERR_PATH = 16, 32, 64
 
@@ -38,7 +38,7 @@ EXPORTS = ("trtv_status_string", "trtv_version", "trtv_subpage_view", "trtv_work
            "trtv_page_table_from_flat", "trtv_workspace_bytes_flat", "trtv_verify_dense_flat",
            "trtv_draft_attn_p32", "trtv_msa_select", "trtv_msa_verify", "trtv_test_withhold_pages",
            "trtv_get_device_error", "trtv_norm_rope_stage", "trtv_workspace_bytes_rows", "trtv_prompt_attn",
-           "trtv_verify_tree", "trtv_tree_commit")
+           "trtv_verify_tree", "trtv_tree_commit", "trtv_read_kv")
 
 
 class TrtvError(RuntimeError):
@@ -136,6 +136,8 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     h.trtv_verify_tree.argtypes = [G, vp, vp, vp, vp, vp, i32, vp, vp, i32, vp, sz, vp]
     h.trtv_tree_commit.restype = ctypes.c_int
     h.trtv_tree_commit.argtypes = [G, vp, vp, vp, vp, vp, vp, i32, vp, vp]
+    h.trtv_read_kv.restype = ctypes.c_int
+    h.trtv_read_kv.argtypes = [G, vp, vp, vp, vp, i32, vp, vp, vp]
     _lib = h
     return h
 
@@ -355,6 +357,8 @@ def _pool_arg(fn: str, geom: Geom, x, dev: int) -> int:
         return x
     need = geom.num_slots * geom.slot_stride * 128 * geom.num_kv_heads * geom.head_dim
     types = (_torch.uint8, _torch.float8_e4m3fn) if geom.kv_dtype == TRTV_FP8_E4M3 else (_torch.bfloat16,)
+    if geom.kv_dtype == TRTV_FP4_E2M1:   # bytes: 4-bit codes and a scale byte for each 16
+        need, types = need * 9 // 16, (_torch.uint8,)
     if x.dtype not in types or x.numel() < need or x.get_device() != dev or not x.is_contiguous():
         _refuse(fn, "kv_pool", x, dev, " or ".join(map(str, types)), (f"{need} elements",))
     return x.data_ptr()
@@ -444,3 +448,17 @@ def trtv_tree_commit(geom: Geom, kv_pool, page_table, kv_lens, qo_indptr, path, 
                                        _arg(fn, "path", path, dev, i32, (b, width)),
                                        _arg(fn, "path_len", path_len, dev, i32, (b,)), width,
                                        _arg(fn, "new_kv_lens", new_kv_lens, dev, i32, (b,)), st))
+
+
+def trtv_read_kv(geom: Geom, kv_pool, page_table, kv_lens, qo_indptr, k_out, v_out, stream=None) -> None:
+    """The packed tokens' cache rows as bf16: k_out, v_out [rows, Hk, D], either may be None."""
+    fn = "trtv_read_kv"
+    dev, st = _begin(stream)
+    if k_out is None and v_out is None:
+        raise ValueError(f"{fn}: k_out and v_out are both None")
+    rows = (v_out if k_out is None else k_out).shape[0]
+    shape = (rows, geom.num_kv_heads, geom.head_dim)
+    pt, kl, ip = _tables(fn, geom, page_table, kv_lens, qo_indptr, dev)
+    _check(fn, load().trtv_read_kv(ctypes.byref(geom), _pool_arg(fn, geom, kv_pool, dev), pt, kl, ip, rows,
+                                   0 if k_out is None else _arg(fn, "k_out", k_out, dev, _torch.bfloat16, shape),
+                                   0 if v_out is None else _arg(fn, "v_out", v_out, dev, _torch.bfloat16, shape), st))

@@ -130,12 +130,13 @@ trtv_status make_plan(const trtv_geom* g, int topk, Plan* pl) {
       g->num_q_heads % g->num_kv_heads != 0 || g->max_pages_per_req < 1 || g->num_slots < 1 ||
       g->slot_stride < 2 || g->num_ctas < 0 || g->num_ctas > kMaxCombineParts)
     return TRTV_ERR_INVALID_ARG;
-  if (g->kv_dtype != TRTV_BF16 && g->kv_dtype != TRTV_FP8_E4M3) return TRTV_ERR_INVALID_ARG;
+  if (g->kv_dtype != TRTV_BF16 && g->kv_dtype != TRTV_FP8_E4M3 && g->kv_dtype != TRTV_FP4_E2M1) return TRTV_ERR_INVALID_ARG;
   if (!(g->sm_scale > 0.f) || !(g->k_scale > 0.f) || !std::isfinite(g->sm_scale) ||
       !std::isfinite(g->k_scale) || !std::isfinite(g->v_scale))
     return TRTV_ERR_INVALID_ARG;
   if (g->head_dim != 64 && g->head_dim != 128) return TRTV_ERR_UNSUPPORTED;
   if (g->kv_dtype == TRTV_FP8_E4M3 && g->head_dim != 128) return TRTV_ERR_UNSUPPORTED;
+  if (g->kv_dtype == TRTV_FP4_E2M1) return TRTV_ERR_UNSUPPORTED;   // trtv_verify_dense and the packed-row calls only
   if (g->qo_len > 32) return TRTV_ERR_UNSUPPORTED;
   if (topk < 0 || topk > 1024) return TRTV_ERR_INVALID_ARG;
   Plan p{};
@@ -601,6 +602,7 @@ const char* trtv_status_string(trtv_status s) {
 int32_t trtv_version(void) { return 100; }
 
 size_t trtv_workspace_bytes(const trtv_geom* geom, int32_t topk) {
+  if (geom != nullptr && geom->kv_dtype == TRTV_FP4_E2M1) return topk == 0 ? ladder_fp4_workspace(geom) : 0;
   Plan pl;
   if (make_plan(geom, topk, &pl) != TRTV_OK) return 0;
   return pl.ws_total;
@@ -627,6 +629,8 @@ trtv_status trtv_subpage_view(const trtv_geom* g, const int32_t* page_table, con
 trtv_status trtv_verify_dense(const trtv_geom* geom, const void* q, const void* kv_pool,
                               const int32_t* page_table, const int32_t* kv_lens, void* out,
                               int32_t out_dtype, void* workspace, size_t ws_bytes, void* stream) {
+  if (geom != nullptr && geom->kv_dtype == TRTV_FP4_E2M1)
+    return ladder_fp4(geom, q, kv_pool, page_table, kv_lens, out, out_dtype, workspace, ws_bytes, stream);
   return attn_common(geom, q, kv_pool, KvIndex{page_table, nullptr, nullptr, nullptr}, kv_lens, nullptr,
                      0, out, out_dtype, workspace, ws_bytes, stream);
 }

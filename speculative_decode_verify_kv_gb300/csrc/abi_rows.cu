@@ -35,7 +35,7 @@ trtv_status rows_geom(const trtv_geom* g, const int32_t* indptr, int32_t num_tok
       g->num_q_heads % g->num_kv_heads != 0 || g->max_pages_per_req < 1 || g->num_slots < 1 || g->slot_stride < 2 ||
       g->num_ctas < 0 || g->num_ctas > kMaxCombineParts)
     return TRTV_ERR_INVALID_ARG;
-  if (g->kv_dtype != TRTV_BF16 && g->kv_dtype != TRTV_FP8_E4M3) return TRTV_ERR_INVALID_ARG;
+  if (g->kv_dtype != TRTV_BF16 && g->kv_dtype != TRTV_FP8_E4M3 && g->kv_dtype != TRTV_FP4_E2M1) return TRTV_ERR_INVALID_ARG;
   if (!(g->sm_scale > 0.f) || !(g->k_scale > 0.f) || !std::isfinite(g->sm_scale) || !std::isfinite(g->k_scale) ||
       !std::isfinite(g->v_scale))
     return TRTV_ERR_INVALID_ARG;
@@ -103,19 +103,21 @@ bool rows_plan(const trtv_geom* g, const RowsGeom& r, RowsPlan* pl) {
   return true;
 }
 
-// Shared memory: Q (one or two tiles), the page ring, E4M3: the codes' ring, the
+// Shared memory: Q (one or two tiles), the page ring, E4M3 and E2M1: the codes' ring, the
 // groups' exchange, the pieces, the requests' scan and its 32 warp totals,
 // barriers.  The ring takes what is left, at most kMaxStages pages.
 constexpr int kMaxStages = 8;
 bool rows_smem(const trtv_geom* g, const RowsPlan& pl, RowsAttnParams* p, size_t* bytes) {
-  const bool fp8 = g->kv_dtype == TRTV_FP8_E4M3;
-  const size_t tile = static_cast<size_t>(kRowsTile) * g->head_dim * 2, raw = static_cast<size_t>(kRowsTile) * g->head_dim;
+  const bool codes = g->kv_dtype != TRTV_BF16;
+  const size_t tile = static_cast<size_t>(kRowsTile) * g->head_dim * 2;
+  const size_t raw = g->kv_dtype == TRTV_FP4_E2M1 ? static_cast<size_t>(kGroups) * kFp4Row * g->head_dim
+                                                  : static_cast<size_t>(kRowsTile) * g->head_dim;
   const size_t scan = align_up((static_cast<size_t>(g->batch) + 1 + 32) * sizeof(int64_t), 16);
   const size_t ml = pl.two ? 0 : 2 * kRowsTile * 2 * sizeof(float);
   const size_t bars = (4 * kMaxStages + 32) * sizeof(uint64_t), pieces = 4 * 48;
   const size_t q = (pl.two ? 2 : 1) * tile;
   const size_t fixed = q + ml + pieces + scan + bars + kAlignSlack;
-  if (fp8) {
+  if (codes) {
     // four converted tiles and three stages of codes where they fit (one-tile
     // items, 64 trees of 16 nodes: 7 % faster than three and five), else three;
     // what is left holds codes in flight
@@ -127,14 +129,14 @@ bool rows_smem(const trtv_geom* g, const RowsPlan& pl, RowsAttnParams* p, size_t
     p->nst = static_cast<int>(std::min<size_t>((kSmemOptin - fixed) / tile, kMaxStages));
     p->nraw = 0;
   }
-  const size_t codes = p->nraw * raw;
+  const size_t raw_ring = p->nraw * raw;
   size_t off = 0;
   p->off_q = 0;
   off += q;
   p->off_ring = static_cast<int>(off);
   off += p->nst * tile;
   p->off_raw = static_cast<int>(off);
-  off += codes;
+  off += raw_ring;
   p->off_ml = static_cast<int>(off);
   off += ml;
   p->off_pieces = static_cast<int>(off);
@@ -195,10 +197,12 @@ trtv_status rows_attn(const trtv_geom* g, const void* q, const void* pool, const
   p.tile_toks = kRowsTile / p.g.group;
   p.items = mask != nullptr && pl.two ? (g->qo_len + 2 * p.tile_toks - 1) / (2 * p.tile_toks) : 1;
   if (p.items > pl.num_ctas) p.items = 1;
-  CUtensorMap kv_map, q_map;
-  if (!encode_pages(g, pool, &kv_map) || !encode_rows(g, p.g, p.tile_toks, q, &q_map)) return TRTV_ERR_CUDA;
+  CUtensorMap kv_map{}, q_map;
+  const bool fp4 = g->kv_dtype == TRTV_FP4_E2M1;
+  if ((!fp4 && !encode_pages(g, pool, &kv_map)) || !encode_rows(g, p.g, p.tile_toks, q, &q_map)) return TRTV_ERR_CUDA;
   uint8_t* wsb = static_cast<uint8_t*>(ws);
   p.tree_mask = mask;
+  p.pool = static_cast<const uint8_t*>(pool);
   p.mask_words = (g->qo_len + 31) / 32;
   p.out = out;
   p.ws_o = reinterpret_cast<float*>(wsb + pl.ws_o);
@@ -207,20 +211,33 @@ trtv_status rows_attn(const trtv_geom* g, const void* q, const void* pool, const
   p.cont = reinterpret_cast<int*>(wsb + pl.ws_cont);
   p.out_f32 = out_dtype == TRTV_F32;
   p.num_ctas = pl.num_ctas;
-  const bool fp8 = g->kv_dtype == TRTV_FP8_E4M3;
-  p.setup = pl.two ? (fp8 ? kRowsSetupTwoFp8 : kRowsSetupTwo) : fp8 ? kRowsSetupOneFp8 : kRowsSetupOne;
+  const bool codes = g->kv_dtype != TRTV_BF16;
+  p.setup = pl.two ? (codes ? kRowsSetupTwoFp8 : kRowsSetupTwo) : codes ? kRowsSetupOneFp8 : kRowsSetupOne;
   p.scale_log2 = g->sm_scale * g->k_scale * 1.4426950408889634f;
   p.v_scale = g->v_scale;
   p.wait_ns = wait_limit_ns();
   p.withhold = withheld_pages();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = fp8 ? launch_rows_attn_fp8(pl.two, kv_map, q_map, p, smem, st)
-                      : launch_rows_attn_bf16(g->head_dim, pl.two, kv_map, q_map, p, smem, st);
+  cudaError_t e = fp4     ? launch_rows_attn_fp4(g->head_dim, pl.two, kv_map, q_map, p, smem, st)
+                  : codes ? launch_rows_attn_fp8(pl.two, kv_map, q_map, p, smem, st)
+                          : launch_rows_attn_bf16(g->head_dim, pl.two, kv_map, q_map, p, smem, st);
   if (e == cudaSuccess) e = launch_rows_join(g->head_dim, pl.two, p, st);
   return e == cudaSuccess ? TRTV_OK : TRTV_ERR_CUDA;
 }
 
 }  // namespace
+
+// The ladder over an E2M1 cache: the packed-row call with qo_len rows per request.
+constexpr int kMaxLadder = 32;
+trtv_status ladder_fp4(const trtv_geom* g, const void* q, const void* pool, const int32_t* page_table,
+                       const int32_t* kv_lens, void* out, int32_t out_dtype, void* ws, size_t ws_bytes, void* stream) {
+  if (g->qo_len > kMaxLadder || g->batch > kMaxBatch) return TRTV_ERR_UNSUPPORTED;
+  if (g->batch < 1 || g->qo_len < 1) return TRTV_ERR_INVALID_ARG;
+  return rows_attn(g, q, pool, page_table, kv_lens, nullptr, g->batch * g->qo_len, nullptr, out, out_dtype, ws, ws_bytes,
+                   stream);
+}
+size_t ladder_fp4_workspace(const trtv_geom* g) { return g->qo_len > kMaxLadder ? 0 : trtv_workspace_bytes_rows(g); }
+
 }  // namespace trtv
 
 using namespace trtv;
@@ -246,7 +263,7 @@ trtv_status trtv_norm_rope_stage(const trtv_geom* g, const trtv_norm_rope* in, c
     return TRTV_ERR_INVALID_ARG;
   if (in->rot_dim > 0 && (in->rope_table == nullptr || in->table_len < 1)) return TRTV_ERR_INVALID_ARG;
   if (in->q == q_out && in->q_stride != qw) return TRTV_ERR_INVALID_ARG;
-  if (g->kv_dtype == TRTV_FP8_E4M3 && g->v_scale == 0.f) return TRTV_ERR_INVALID_ARG;   // values are divided by it
+  if (g->kv_dtype != TRTV_BF16 && g->v_scale == 0.f) return TRTV_ERR_INVALID_ARG;   // values are divided by it
   const void* ptrs[] = {in->q, in->k, in->v, in->q_weight, in->k_weight, in->rope_table, q_out, kv_pool};
   for (const void* x : ptrs)
     if (!aligned(x, 16)) return TRTV_ERR_INVALID_ARG;
@@ -282,7 +299,7 @@ trtv_status trtv_norm_rope_stage(const trtv_geom* g, const trtv_norm_rope* in, c
   const int chunks = static_cast<int>(std::min<int64_t>(want, (heads + batch_rows - 1) / batch_rows));
   p.heads_per_warp = ((heads + chunks - 1) / chunks + batch_rows - 1) / batch_rows * batch_rows;
   p.chunks = (heads + p.heads_per_warp - 1) / p.heads_per_warp;
-  const cudaError_t e = launch_norm_rope_stage(D, g->kv_dtype == TRTV_FP8_E4M3, p, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_norm_rope_stage(D, g->kv_dtype, p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? TRTV_OK : TRTV_ERR_CUDA;
 }
 
@@ -313,6 +330,23 @@ trtv_status trtv_verify_tree(const trtv_geom* g, const void* q, const void* kv_p
                    ws_bytes, stream);
 }
 
+trtv_status trtv_read_kv(const trtv_geom* g, const void* kv_pool, const int32_t* page_table, const int32_t* kv_lens,
+                         const int32_t* qo_indptr, int32_t num_tokens, void* k_out, void* v_out, void* stream) {
+  ReadParams p{};
+  trtv_status s = rows_geom(g, qo_indptr, num_tokens, &p.g);
+  if (s != TRTV_OK || num_tokens == 0) return s;
+  if (kv_pool == nullptr || (k_out == nullptr && v_out == nullptr)) return TRTV_ERR_INVALID_ARG;
+  if (!aligned(kv_pool, 16) || !aligned(k_out, 16) || !aligned(v_out, 16)) return TRTV_ERR_INVALID_ARG;
+  if ((s = rows_device(&p.g, page_table, kv_lens)) != TRTV_OK) return s;
+  p.pool = static_cast<const uint8_t*>(kv_pool);
+  p.k_out = static_cast<__nv_bfloat16*>(k_out);
+  p.v_out = static_cast<__nv_bfloat16*>(v_out);
+  p.k_scale = g->k_scale;
+  p.v_scale = g->v_scale;
+  const cudaError_t e = launch_read_kv(g->head_dim, g->kv_dtype, p, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? TRTV_OK : TRTV_ERR_CUDA;
+}
+
 trtv_status trtv_tree_commit(const trtv_geom* g, void* kv_pool, const int32_t* page_table, const int32_t* kv_lens,
                              const int32_t* qo_indptr, const int32_t* path, const int32_t* path_len,
                              int32_t max_path, int32_t* new_kv_lens, void* stream) {
@@ -331,7 +365,7 @@ trtv_status trtv_tree_commit(const trtv_geom* g, void* kv_pool, const int32_t* p
   p.new_kv_lens = new_kv_lens;
   p.max_path = max_path;
   p.row_bytes = g->head_dim * (g->kv_dtype == TRTV_FP8_E4M3 ? 1 : 2);
-  const cudaError_t e = launch_tree_commit(p, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_tree_commit(g->head_dim, g->kv_dtype, p, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? TRTV_OK : TRTV_ERR_CUDA;
 }
 

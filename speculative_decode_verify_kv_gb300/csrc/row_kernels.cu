@@ -49,8 +49,30 @@ __device__ __forceinline__ uint32_t pack4_e4m3(const float (&x)[4], float scale)
   return lo | (hi << 16);
 }
 
-template <int D, bool FP8, bool INTER>
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// Eight E2M1 codes of t / s, nearest even, saturated to +-6, the first in the lowest bits.
+__device__ __forceinline__ uint32_t pack8_e2m1(const float (&t)[8], float s) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(t[0] / s), "f"(t[1] / s), "f"(t[2] / s), "f"(t[3] / s), "f"(t[4] / s), "f"(t[5] / s), "f"(t[6] / s), "f"(t[7] / s));
+  return r;
+}
+
+template <int D, int KV, bool INTER>
 __global__ void __launch_bounds__(kStageThreads) norm_rope_stage_kernel(const __grid_constant__ NormRopeParams p) {
+  constexpr bool FP8 = KV == TRTV_FP8_E4M3, FP4 = KV == TRTV_FP4_E2M1;
+  // E2M1: a head's values change lanes here, so that two neighbours hold 16 dims in order
+  __shared__ __align__(16) float swap[FP4 ? kStageThreads / 32 : 1][FP4 ? 32 * 8 : 1];
   constexpr int LPR = D / 8;         // lanes per row
   constexpr int GPW = 32 / LPR;      // rows a warp holds at a time
   const RowsGeom& g = p.g;
@@ -127,8 +149,10 @@ __global__ void __launch_bounds__(kStageThreads) norm_rope_stage_kernel(const __
     wk[1] = *reinterpret_cast<const uint2*>(p.k_weight + db);
   }
   __nv_bfloat16* const qd = p.q_out + static_cast<int64_t>(tok) * nq * D;
-  const int64_t kd = cell_offset(g, slot < 0 ? 0 : slot, live ? cell : 0, D) - static_cast<int64_t>(nq) * kSub * D;
-  const int64_t vd = kd + static_cast<int64_t>(kGroups - 1) * g.num_kv_heads * kSub * D;   // (one page buffer on, Hk heads later)
+  constexpr int64_t kHead = FP4 ? kFp4Row * D : kSub * D;   // elements (E2M1: bytes) from one head's rows to the next's
+  const int64_t kd = (FP4 ? fp4_block(g, slot < 0 ? 0 : slot, live ? cell : 0, D) : cell_offset(g, slot < 0 ? 0 : slot, live ? cell : 0, D)) -
+                     nq * kHead;
+  const int64_t vd = kd + static_cast<int64_t>(kGroups - 1) * g.num_kv_heads * kHead;   // (one page buffer on, Hk heads later)
   auto process = [&](int h, const Rows& x) {
 #pragma unroll
     for (int r = 0; r < kStageRows; ++r) {
@@ -143,7 +167,7 @@ __global__ void __launch_bounds__(kStageThreads) norm_rope_stage_kernel(const __
       for (int i = 0; i < 4; ++i) ss += a[i] * a[i] + c[i] * c[i];
 #pragma unroll
       for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (hr >= h1) continue;
+      if (!FP4 && hr >= h1) continue;
       if (!is_v) {
         if ((is_q ? p.q_weight : p.k_weight) != nullptr) {
           const float f = rsqrtf(ss * (1.f / D) + p.eps);
@@ -175,11 +199,36 @@ __global__ void __launch_bounds__(kStageThreads) norm_rope_stage_kernel(const __
           }
         }
       }
+      if constexpr (FP4) {
+        if (__any_sync(0xffffffffu, hr < h1 && !is_q && slot >= 0)) {
+          float* row = swap[threadIdx.x >> 5] + sub * D;
+          *reinterpret_cast<float4*>(row + da) = make_float4(a[0], a[1], a[2], a[3]);
+          *reinterpret_cast<float4*>(row + db) = make_float4(c[0], c[1], c[2], c[3]);
+          __syncwarp();
+          const float4 x0 = *reinterpret_cast<const float4*>(row + 8 * l), x1 = *reinterpret_cast<const float4*>(row + 8 * l + 4);
+          __syncwarp();
+          const float scale = is_v ? p.v_scale : p.k_scale;
+          const float t[8] = {x0.x / scale, x0.y / scale, x0.z / scale, x0.w / scale, x1.x / scale, x1.y / scale, x1.z / scale, x1.w / scale};
+          float top = fabsf(t[0]);
+#pragma unroll
+          for (int i = 1; i < 8; ++i) top = max_nan(top, fabsf(t[i]));
+          top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          const __nv_fp8_storage_t s8 = __nv_cvt_float_to_fp8(top / 6.f, __NV_SATFINITE, __NV_E4M3);
+          const float s = __half2float(__half(__nv_cvt_fp8_to_halfraw(s8, __NV_E4M3)));
+          if (hr < h1 && !is_q && slot >= 0) {
+            uint8_t* blk = static_cast<uint8_t*>(p.pool) + (is_v ? vd : kd) + hr * kHead;
+            const int row_in = cell % kSub;
+            *reinterpret_cast<uint32_t*>(blk + row_in * (D / 2) + 4 * l) = s > 0.f ? pack8_e2m1(t, s) : 0u;
+            if ((l & 1) == 0) blk[kSub * (D / 2) + row_in * (D / 16) + l / 2] = s8;
+          }
+        }
+        if (hr >= h1) continue;
+      }
       if (is_q) {
         __nv_bfloat16* dst = qd + hr * D;
         *reinterpret_cast<uint2*>(dst + da) = live ? pack4(a) : make_uint2(0, 0);
         *reinterpret_cast<uint2*>(dst + db) = live ? pack4(c) : make_uint2(0, 0);
-      } else if (slot >= 0) {
+      } else if (!FP4 && slot >= 0) {
         const int64_t off = (is_v ? vd : kd) + static_cast<int64_t>(hr) * kSub * D;
         if constexpr (FP8) {
           const float scale = is_v ? p.v_scale : p.k_scale;
@@ -203,18 +252,114 @@ __global__ void __launch_bounds__(kStageThreads) norm_rope_stage_kernel(const __
   }
 }
 
-cudaError_t launch_norm_rope_stage(int head_dim, bool fp8, const NormRopeParams& p, cudaStream_t st) {
+template <int D, int KV>
+cudaError_t launch_stage_kind(bool interleaved, dim3 grid, dim3 block, const NormRopeParams& p, cudaStream_t st) {
+  return interleaved ? launch_pdl(norm_rope_stage_kernel<D, KV, true>, grid, block, 0, st, p)
+                     : launch_pdl(norm_rope_stage_kernel<D, KV, false>, grid, block, 0, st, p);
+}
+
+cudaError_t launch_norm_rope_stage(int head_dim, int kv_dtype, const NormRopeParams& p, cudaStream_t st) {
   const int64_t warps = static_cast<int64_t>(p.chunks) * p.g.num_tokens;
   const int64_t blocks = (warps + kStageThreads / 32 - 1) / (kStageThreads / 32);
   const dim3 grid(static_cast<unsigned>(blocks)), block(kStageThreads);
-  if (p.interleaved) {
-    if (fp8) return launch_pdl(norm_rope_stage_kernel<128, true, true>, grid, block, 0, st, p);
-    return head_dim == 64 ? launch_pdl(norm_rope_stage_kernel<64, false, true>, grid, block, 0, st, p)
-                          : launch_pdl(norm_rope_stage_kernel<128, false, true>, grid, block, 0, st, p);
+  const bool inter = p.interleaved != 0;
+  if (kv_dtype == TRTV_FP8_E4M3) return launch_stage_kind<128, TRTV_FP8_E4M3>(inter, grid, block, p, st);
+  if (kv_dtype == TRTV_FP4_E2M1)
+    return head_dim == 64 ? launch_stage_kind<64, TRTV_FP4_E2M1>(inter, grid, block, p, st)
+                          : launch_stage_kind<128, TRTV_FP4_E2M1>(inter, grid, block, p, st);
+  return head_dim == 64 ? launch_stage_kind<64, TRTV_BF16>(inter, grid, block, p, st)
+                        : launch_stage_kind<128, TRTV_BF16>(inter, grid, block, p, st);
+}
+
+// ---------------------------------------------------------------------------
+// Reading rows back.  The cache rows of the packed tokens as bf16: a warp per
+// token, 8 elements a lane and step.  A value is code x block scale (exact in
+// binary32) x the tensor's scale, rounded to binary32 and then to bf16.  Bound by
+// its bytes.
+constexpr int kReadThreads = 128;
+
+template <int D, int KV>
+__global__ void __launch_bounds__(kReadThreads) read_kv_kernel(const __grid_constant__ ReadParams p) {
+  constexpr int LPR = D / 8;         // lanes per row
+  const RowsGeom& g = p.g;
+  const int lane = threadIdx.x & 31;
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0) check_spans(g);
+  const int64_t tok64 = static_cast<int64_t>(blockIdx.x) * (kReadThreads / 32) + (threadIdx.x >> 5);
+  if (tok64 >= g.num_tokens) return;
+  const int tok = static_cast<int>(tok64);
+  RowSpan span;
+  const int b = row_owner(g, tok, lane, span);
+  if (b >= g.batch) return;   // nobody's row
+  const int L = g.kv_lens[b];
+  const bool len_ok = len_valid(L, span.n, g.max_pages);
+  const int cell = len_ok ? L - span.n + (tok - span.row0) : 0;
+  int slot = -1;
+  if (len_ok) {
+    slot = g.page_table[static_cast<int64_t>(b) * g.max_pages + cell / kPage];
+    if (slot < 0 || slot >= g.num_slots) {
+      slot = -1;
+      if (lane == 0) atomicOr(g.err, TRTV_DEVERR_PAGE_ID);
+    }
+  } else if (lane == 0) {
+    atomicOr(g.err, TRTV_DEVERR_KV_LEN);
   }
-  if (fp8) return launch_pdl(norm_rope_stage_kernel<128, true, false>, grid, block, 0, st, p);
-  return head_dim == 64 ? launch_pdl(norm_rope_stage_kernel<64, false, false>, grid, block, 0, st, p)
-                        : launch_pdl(norm_rope_stage_kernel<128, false, false>, grid, block, 0, st, p);
+  const int hk = g.num_kv_heads, row_in = cell % kSub;
+  constexpr int64_t kHead = KV == TRTV_FP4_E2M1 ? kFp4Row * D : kSub * D;   // elements (E2M1: bytes) between heads
+  const int64_t base = KV == TRTV_FP4_E2M1 ? fp4_block(g, slot < 0 ? 0 : slot, cell, D) : cell_offset(g, slot < 0 ? 0 : slot, cell, D);
+#pragma unroll 4
+  for (int i = lane; i < 2 * hk * LPR; i += 32) {
+    const int hv = i / LPR, l = i % LPR;
+    const bool is_v = hv >= hk;
+    __nv_bfloat16* dst = is_v ? p.v_out : p.k_out;
+    if (dst == nullptr) continue;
+    dst += (static_cast<int64_t>(tok) * hk + (is_v ? hv - hk : hv)) * D + 8 * l;
+    // (a V head lies one page buffer, 4 hk heads' rows, on)
+    const int64_t off = base + (is_v ? static_cast<int64_t>(hv - hk) + static_cast<int64_t>(kGroups) * hk : hv) * kHead;
+    uint4 o = make_uint4(0, 0, 0, 0);
+    if (slot >= 0) {
+      const float scale = is_v ? p.v_scale : p.k_scale;
+      if constexpr (KV == TRTV_BF16) {
+        o = *reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.pool) + off + 8 * l);
+      } else {
+        uint32_t h[4];
+        float s = scale, blk = 1.f;
+        if constexpr (KV == TRTV_FP8_E4M3) {
+          const uint2 w = *reinterpret_cast<const uint2*>(p.pool + off + 8 * l);
+          h[0] = e4m3x2_to_f16x2_reg(w.x);
+          h[1] = e4m3x2_to_f16x2_reg(w.x >> 16);
+          h[2] = e4m3x2_to_f16x2_reg(w.y);
+          h[3] = e4m3x2_to_f16x2_reg(w.y >> 16);
+        } else {
+          const uint8_t* blkp = p.pool + off;
+          e2m1x8_to_f16x8(*reinterpret_cast<const uint32_t*>(blkp + row_in * (D / 2) + 4 * l), h);
+          const uint32_t sc = e4m3x2_to_f16x2_reg(blkp[kSub * (D / 2) + row_in * (D / 16) + l / 2]);
+          blk = __half2float(__ushort_as_half(static_cast<unsigned short>(sc & 0xffff)));
+        }
+        float f[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
+          f[2 * k] = v.x * blk * s;
+          f[2 * k + 1] = v.y * blk * s;
+        }
+        o = make_uint4(pack2<false>(f[0], f[1]), pack2<false>(f[2], f[3]), pack2<false>(f[4], f[5]), pack2<false>(f[6], f[7]));
+      }
+    }
+    *reinterpret_cast<uint4*>(dst) = o;
+  }
+}
+
+cudaError_t launch_read_kv(int head_dim, int kv_dtype, const ReadParams& p, cudaStream_t st) {
+  const int warps = kReadThreads / 32;
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(p.g.num_tokens) + warps - 1) / warps)), block(kReadThreads);
+  if (kv_dtype == TRTV_FP8_E4M3) return launch_pdl(read_kv_kernel<128, TRTV_FP8_E4M3>, grid, block, 0, st, p);
+  if (kv_dtype == TRTV_FP4_E2M1)
+    return head_dim == 64 ? launch_pdl(read_kv_kernel<64, TRTV_FP4_E2M1>, grid, block, 0, st, p)
+                          : launch_pdl(read_kv_kernel<128, TRTV_FP4_E2M1>, grid, block, 0, st, p);
+  return head_dim == 64 ? launch_pdl(read_kv_kernel<64, TRTV_BF16>, grid, block, 0, st, p)
+                        : launch_pdl(read_kv_kernel<128, TRTV_BF16>, grid, block, 0, st, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -229,8 +374,11 @@ constexpr int kCommitThreads = 256;
 constexpr int kMaxTree = 128;
 constexpr int kMove = 8;
 
+// E2M1 caches (D = head_dim, else 0): columns of 4 bytes, a row's codes and its scales.
+template <int D>
 __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const __grid_constant__ CommitParams p) {
-  __shared__ int64_t src[kMaxTree], dst[kMaxTree];  // 16-byte units, column 0
+  __shared__ int64_t src[kMaxTree], dst[kMaxTree];  // 16-byte units, column 0 (E2M1: 4-byte units, KV head 0's block)
+  __shared__ int from[D != 0 ? kMaxTree : 1];       // E2M1: the source's row of its block
   __shared__ int bad, first;
   const RowsGeom& g = p.g;
   const int b = blockIdx.x, tid = threadIdx.x;
@@ -261,8 +409,14 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const __gri
         if (t <= before || t >= n) {
           atomicOr(&bad, TRTV_DEVERR_PATH);
         } else {
-          src[tid] = cell_offset(g, table[(ctx + t) / kPage], ctx + t, D16);
-          dst[tid] = cell_offset(g, table[(ctx + tid) / kPage], ctx + tid, D16);
+          if constexpr (D == 0) {
+            src[tid] = cell_offset(g, table[(ctx + t) / kPage], ctx + t, D16);
+            dst[tid] = cell_offset(g, table[(ctx + tid) / kPage], ctx + tid, D16);
+          } else {
+            src[tid] = fp4_block(g, table[(ctx + t) / kPage], ctx + t, D) / 4;
+            dst[tid] = fp4_block(g, table[(ctx + tid) / kPage], ctx + tid, D) / 4;
+            from[tid] = (ctx + t) % kSub;
+          }
           if (t != tid) atomicMin(&first, tid);
         }
       }
@@ -275,6 +429,27 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const __gri
     p.new_kv_lens[b] = e != 0 || n == 0 ? L : ctx + k;
   }
   if (bad != 0 || n == 0) return;
+  if constexpr (D != 0) {
+    constexpr int CODE = D / 8, SCALE = D / 64, BLOCK = kFp4Row * D / 4;   // 4-byte columns of a row; units of a block
+    const int64_t page = static_cast<int64_t>(kGroups) * g.num_kv_heads * BLOCK;
+    uint32_t* pool = reinterpret_cast<uint32_t*>(p.pool);
+    const int cols = 2 * g.num_kv_heads * (CODE + SCALE);
+    for (int c = tid; c < cols; c += kCommitThreads) {
+      const int hv = c / (CODE + SCALE), w = c % (CODE + SCALE);
+      const int64_t col = (hv & 1) * page + static_cast<int64_t>(hv >> 1) * BLOCK + (w < CODE ? w : kSub * CODE + w - CODE);
+      const int pitch = w < CODE ? CODE : SCALE;
+      for (int i = first; i < k; i += kMove) {
+        uint32_t v[kMove];
+#pragma unroll
+        for (int u = 0; u < kMove; ++u)
+          if (i + u < k) v[u] = pool[src[i + u] + col + from[i + u] * pitch];
+#pragma unroll
+        for (int u = 0; u < kMove; ++u)
+          if (i + u < k) pool[dst[i + u] + col + (ctx + i + u) % kSub * pitch] = v[u];
+      }
+    }
+    return;
+  }
   const int D16 = p.row_bytes / 16;
   const int64_t page = static_cast<int64_t>(kGroups) * g.num_kv_heads * kSub * D16;
   uint4* pool = reinterpret_cast<uint4*>(p.pool);
@@ -294,8 +469,11 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const __gri
   }
 }
 
-cudaError_t launch_tree_commit(const CommitParams& p, cudaStream_t st) {
-  return launch_pdl(tree_commit_kernel, dim3(p.g.batch), dim3(kCommitThreads), 0, st, p);
+cudaError_t launch_tree_commit(int head_dim, int kv_dtype, const CommitParams& p, cudaStream_t st) {
+  const dim3 grid(p.g.batch), block(kCommitThreads);
+  if (kv_dtype != TRTV_FP4_E2M1) return launch_pdl(tree_commit_kernel<0>, grid, block, 0, st, p);
+  return head_dim == 64 ? launch_pdl(tree_commit_kernel<64>, grid, block, 0, st, p)
+                        : launch_pdl(tree_commit_kernel<128>, grid, block, 0, st, p);
 }
 
 }  // namespace trtv

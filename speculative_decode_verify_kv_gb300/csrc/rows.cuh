@@ -114,6 +114,42 @@ struct CommitParams {
   int max_path, row_bytes;  // bytes of one head's row in the cache
 };
 
+struct ReadParams {
+  RowsGeom g;
+  const uint8_t* pool;
+  __nv_bfloat16* k_out;     // [num_tokens, KV heads, head_dim], or null
+  __nv_bfloat16* v_out;
+  float k_scale, v_scale;
+};
+
+// E2M1 caches: a page buffer is [4 groups][KV heads] blocks of kFp4Row * head_dim
+// bytes: 32 rows of head_dim / 2 bytes of codes (the even dim in the low half),
+// then 32 rows of head_dim / 16 E4M3 scales, one for each 16 dims.
+constexpr int kFp4Row = kSub / 2 + kSub / 16;
+
+// Byte offset of KV head 0's block that holds cache position `pos`, in slot s's K page.
+__device__ __forceinline__ int64_t fp4_block(const RowsGeom& g, int64_t s, int pos, int D) {
+  return (s * g.slot_stride * kGroups + (pos % kPage) / kSub) * g.num_kv_heads * static_cast<int64_t>(kFp4Row * D);
+}
+
+// four E4M3 codes' pairs and eight E2M1 codes -> f16 (exact), and a product of f16 pairs
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2_reg(uint32_t two) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(r) : "r"(two));
+  return r;
+}
+__device__ __forceinline__ void e2m1x8_to_f16x8(uint32_t w, uint32_t (&o)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
+      : "r"(w));
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 constexpr int kRowsTile = 128;   // rows of one UMMA tile of the attention
 
 // A row-tile item of the attention that the stream-K split cut: written by the
@@ -126,6 +162,7 @@ struct __align__(16) RowsSplit {
 struct RowsAttnParams {
   RowsGeom g;
   const uint32_t* tree_mask;   // [num_tokens, mask_words] or null: the causal bound
+  const uint8_t* pool;         // E2M1 caches (others: the tensor map)
   void* out;
   float* ws_o;                 // [2 * num_ctas, rows, D] pieces, each normalised by its own sum
   float* ws_lse;               // [2 * num_ctas, rows] log2 of their sums
@@ -148,8 +185,11 @@ cudaError_t launch_rows_attn_bf16(int head_dim, bool two, const CUtensorMap& kv_
                                   const RowsAttnParams& p, size_t smem, cudaStream_t st);
 cudaError_t launch_rows_attn_fp8(bool two, const CUtensorMap& kv_map, const CUtensorMap& q_map,
                                  const RowsAttnParams& p, size_t smem, cudaStream_t st);
+cudaError_t launch_rows_attn_fp4(int head_dim, bool two, const CUtensorMap& kv_map, const CUtensorMap& q_map,
+                                 const RowsAttnParams& p, size_t smem, cudaStream_t st);
 cudaError_t launch_rows_join(int head_dim, bool two, const RowsAttnParams& p, cudaStream_t st);
-cudaError_t launch_norm_rope_stage(int head_dim, bool fp8, const NormRopeParams& p, cudaStream_t st);
-cudaError_t launch_tree_commit(const CommitParams& p, cudaStream_t st);
+cudaError_t launch_read_kv(int head_dim, int kv_dtype, const ReadParams& p, cudaStream_t st);
+cudaError_t launch_norm_rope_stage(int head_dim, int kv_dtype, const NormRopeParams& p, cudaStream_t st);
+cudaError_t launch_tree_commit(int head_dim, int kv_dtype, const CommitParams& p, cudaStream_t st);
 
 }  // namespace trtv

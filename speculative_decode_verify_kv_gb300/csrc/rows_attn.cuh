@@ -1,6 +1,6 @@
 // rows_attn.cuh -- attention of packed token rows over the paged cache on the
 // tcgen05 tensor cores: prompts (causal) and drafted trees (a bit mask among
-// the new tokens).  head_dim 64 or 128, bf16 or E4M3 K/V, any group <= 128.
+// the new tokens).  head_dim 64 or 128, bf16, E4M3 or E2M1 K/V, any group <= 128.
 //
 // Work.  A 128-row tile is tile_toks = 128 / G tokens times the G query heads
 // of one KV head (row = t G + g), so every K/V byte a CTA loads serves the whole
@@ -38,6 +38,9 @@
 // 2^-25 were lost: 0.4 % of the sum in a row of one large and 131072 small).  A
 // reference that moves at 2^4, with a lift of 2^10, takes 2242 us where logits have a
 // deviation of 6 (a prompt of 16384), 2206 so.
+//
+// E2M1 caches: the same, a code times its block's E4M3 scale being exact in f16
+// (at most 6 significant bits, magnitudes 2^-10 .. 2688).
 //
 // What bounds a prompt's page is one group's chain: softmax, then PV and the
 // next QK, which cannot start before P is written over S.  So a row's scores are
@@ -265,6 +268,22 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32
       : "r"(w));
 }
 
+// Bytes [src, src + bytes) of global memory, both ends and dst 16-byte aligned.
+template <bool ONCE>
+__device__ __forceinline__ void bulk_load(void* dst, const uint8_t* src, int bytes, uint64_t* bar, uint64_t evict_first) {
+  if constexpr (ONCE) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+            smem_u32(dst)),
+        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(evict_first)
+        : "memory");
+  } else {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+  }
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -446,16 +465,19 @@ __device__ __forceinline__ void store_sector(uint8_t* dst, bool wide, const uint
   }
 }
 
-template <int D, bool FP8, bool TWO, bool LANES>
-__global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
+template <int D, int KV, bool TWO, bool LANES>
+__global__ void __launch_bounds__(KV != TRTV_BF16 ? 512 : 384, 1)
     rows_attn_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ CUtensorMap q_map,
                      const __grid_constant__ RowsAttnParams p) {
   static_assert(D == 64 || D == 128, "head_dim 64 or 128");
-  static_assert(!FP8 || D == 128, "E4M3 caches: head_dim 128");
+  static_assert(KV != TRTV_FP8_E4M3 || D == 128, "E4M3 caches: head_dim 128");
+  constexpr bool CODES = KV != TRTV_BF16;           // codes, turned into f16 tiles
+  constexpr bool FP4 = KV == TRTV_FP4_E2M1;
+  constexpr int GROUPS4 = kFp4Row * D;              // E2M1: bytes of 32 rows of one head, codes and scales
   constexpr int HB = D / 64;                        // 64-column blocks of a 16-bit tile
   constexpr int TILE = kRowsTile * D * 2;           // bytes of a Q, K or V tile in 16 bits
-  constexpr int RAW = kRowsTile * D;                // of a page of codes
-  constexpr uint32_t FMT = FP8 ? 0u : (1u << 7) | (1u << 10);   // f16 or bf16 operands
+  constexpr int RAW = FP4 ? GROUPS4 * kGroups : kRowsTile * D;   // of a page of codes
+  constexpr uint32_t FMT = CODES ? 0u : (1u << 7) | (1u << 10);   // f16 or bf16 operands
   constexpr uint32_t IDESC_QK = (1u << 4) | FMT | ((128u >> 3) << 17) | ((128u >> 4) << 24);
   constexpr uint32_t IDESC_PV = (1u << 4) | FMT | (1u << 16) | ((static_cast<uint32_t>(D) >> 3) << 17) |
                                 ((128u >> 4) << 24);
@@ -491,7 +513,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
 
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
-      mbar_init(&full[i], FP8 ? kConvertWarps : 1);
+      mbar_init(&full[i], CODES ? kConvertWarps : 1);
       mbar_init(&empty[i], TWO ? 2 : 1);   // the groups' issuers that read the page
     }
     for (int i = 0; i < NRAW; ++i) {
@@ -509,7 +531,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
     }
     for (int i = 0; i < kRowsPieces; ++i) {
       mbar_init(&ifull[i], 1);
-      mbar_init(&iempty[i], 9 + (TWO ? 2 : 1) + (FP8 ? 4 : 0));   // softmax 8, page loads, UMMA issue, conversion 4
+      mbar_init(&iempty[i], 9 + (TWO ? 2 : 1) + (CODES ? 4 : 0));   // softmax 8, page loads, UMMA issue, conversion 4
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&turn[i], 1);
@@ -578,7 +600,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------ page loads
-    if (lane == 0) prefetch_tensormap(&kv_map);
+    if (!FP4 && lane == 0) prefetch_tensormap(&kv_map);
     const int64_t vbuf = kGroups;
     const uint64_t pol = policy_evict_first();
     RowsPiece it{};
@@ -617,13 +639,22 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         if (stop) break;
         ++npg;
         for (int kv = 0; kv < 2 && ok; ++kv, ++i) {
-          if constexpr (FP8) {
+          if constexpr (CODES) {
             const int st = i % NRAW;
             if (lane == 0) {
               if (i >= NRAW) ok = rows_wait(&rawfree[st], static_cast<uint32_t>(i / NRAW - 1) & 1u, wt);
               if (ok) {
-                mbar_arrive_expect_tx(&raw[st], RAW);
-                tma_load_page<!TWO>(rring + st * RAW, &kv_map, &raw[st], 0, it.h, static_cast<int>(sub + kv * vbuf), pol);
+                if constexpr (FP4) {   // the sub-pages that hold positions below kv_len
+                  const int used = min(kGroups, (it.ctx + it.n - j * kPage + kSub - 1) / kSub);
+                  const int64_t pitch = static_cast<int64_t>(g.num_kv_heads) * GROUPS4;
+                  const uint8_t* src = p.pool + (sub + kv * vbuf) * pitch + static_cast<int64_t>(it.h) * GROUPS4;
+                  mbar_arrive_expect_tx(&raw[st], used * GROUPS4);
+                  for (int gr = 0; gr < used; ++gr)
+                    bulk_load<!TWO>(rring + st * RAW + gr * GROUPS4, src + gr * pitch, GROUPS4, &raw[st], pol);
+                } else {
+                  mbar_arrive_expect_tx(&raw[st], RAW);
+                  tma_load_page<!TWO>(rring + st * RAW, &kv_map, &raw[st], 0, it.h, static_cast<int>(sub + kv * vbuf), pol);
+                }
               }
             }
           } else {
@@ -645,8 +676,8 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
     }
     // never leave copies in flight
     if (lane == 0) {
-      const int depth = FP8 ? NRAW : NST;
-      uint64_t* bars = FP8 ? raw : full;
+      const int depth = CODES ? NRAW : NST;
+      uint64_t* bars = CODES ? raw : full;
       if (!ok) --i;   // the load that gave up was not issued
       for (int k = (i > depth ? i - depth : 0); k < i; ++k) mbar_drain(&bars[k % depth], static_cast<uint32_t>(k / depth) & 1u, wt);
     }
@@ -764,7 +795,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
       const int j0 = it.j0, s0 = TWO ? warp - 9 : 0, e = s0 == 0 ? it.e0 : it.e1;
       const int slot = TWO ? s0 : 0, lead = TWO ? 1 : 2;   // QK runs `lead` pages ahead of PV
       if (j0 < e) {
-        wait1(FP8 ? &qconv[slot] : &qfull[slot], (qph >> slot) & 1u);
+        wait1(CODES ? &qconv[slot] : &qfull[slot], (qph >> slot) & 1u);
         qph ^= 1u << slot;
       }
 #pragma unroll 1
@@ -774,7 +805,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         const bool page = j >= j0, pv = page && j < e, next = j + lead < it.j1, qk = j + lead < e;
         if (page) {
           wait1(&full[vst], vph);
-          if constexpr (!FP8) {
+          if constexpr (!CODES) {
             const int live = it.ctx + it.n - j * kPage;   // V rows past kv_len are zeroed (TWO: by both groups alike)
             if (live < kPage && alive) {
               for (int c = lane; c < (kPage - live) * 8; c += 32)
@@ -832,13 +863,13 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
     umma_commit_elect(&mdone[warp - 9]);
     if (lane == 0) mbar_drain(&mdone[warp - 9], 0, wt);
     __syncwarp();
-  } else if (FP8 && warp >= 12) {
+  } else if (CODES && warp >= 12) {
     // -------------------------------------------------- E4M3 codes -> f16 tiles
     // All four warps work on each tile (a tile each would put two waits per
     // stage use out of order).  Sixteen threads take rows r and r ^ 5 of an 8-row block:
     // with the tiles' swizzle (16-byte chunk c of row r at c ^ (r % 8)) every
     // eight lanes' loads and stores then fall into eight different bank groups.
-    if constexpr (FP8) {
+    if constexpr (KV == TRTV_FP8_E4M3) {
       constexpr int TT = 32 * kConvertWarps, PER = kRowsTile * 8 / TT;   // 16-byte chunks a thread takes of a tile
       const int ct = tid - 384;
       const int c = (ct & 3) + 4 * ((ct >> 3) & 1), odd = (ct >> 2) & 1 ? 5 : 0, g0 = ct >> 4;
@@ -899,6 +930,74 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         }
       }
     }
+    if constexpr (FP4) {
+      // A thread takes 16-byte chunks of codes, 32 head dims each with two scales.
+      // Four consecutive rows' lanes take chunks 0, 1 of two rows and 2, 3 of the
+      // others (then the other way round): eight lanes' loads fall into eight bank
+      // groups, and so do their stores into the swizzled tile.
+      constexpr int PER = D / 32;      // chunks a thread takes of a tile
+      const int w = warp - 12, y = (lane >> 1) & 3;
+      const int c = D == 128 ? 2 * ((y >> 1) ^ ((lane >> 3) & 1)) + (lane & 1) : lane & 1;
+      const int r0 = D == 128 ? 8 * w + 4 * (lane >> 4) + y : 16 * w + (lane >> 1);   // row of the tile, of chunk k: r0 + STEP k
+      constexpr int STEP = kRowsTile / PER;
+      int rs = 0, st = 0;              // stages of the codes and of the tile
+      uint32_t rph = 0, sph = 1;       // parities: codes landed, stage free (the first round is)
+      bool ok = true;
+      RowsPiece it;
+      while (ok && next_piece(it)) {
+        for (int x = 2 * it.j0; x < 2 * it.j1; ++x) {
+          ok = __all_sync(0xffffffffu, rows_wait(&raw[rs], rph, wt));
+          if (!ok) break;
+          const uint8_t* src = rring + rs * RAW;
+          uint8_t* dst = ring + st * TILE + (c >> 1) * (TILE / HB);
+          uint4 v[PER];
+          uint32_t sc[PER];
+          const int live = x & 1 ? it.ctx + it.n - (x >> 1) * kPage : kPage;   // V rows past kv_len are zeroed
+#pragma unroll
+          for (int k = 0; k < PER; ++k) {
+            const int r = r0 + STEP * k;
+            const uint8_t* blk = src + (r / kSub) * GROUPS4;
+            v[k] = *reinterpret_cast<const uint4*>(blk + (r % kSub) * (D / 2) + c * 16);
+            sc[k] = *reinterpret_cast<const uint16_t*>(blk + kSub * (D / 2) + (r % kSub) * (D / 16) + c * 2);
+            if (r >= live) {
+              v[k] = make_uint4(0, 0, 0, 0);
+              sc[k] = 0;
+            }
+          }
+          ok = __all_sync(0xffffffffu, rows_wait(&empty[st], sph, wt));
+          if (!ok) break;
+#pragma unroll
+          for (int k = 0; k < PER; ++k) {
+            const int r = r0 + STEP * k;
+            const uint32_t two = e4m3x2_to_f16x2_reg(sc[k]);
+            const uint32_t s[2] = {__byte_perm(two, 0, 0x1010), __byte_perm(two, 0, 0x3232)};
+            const uint32_t in[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t o[4];
+              e2m1x8_to_f16x8(in[i], o);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[e] = mul_f16x2(o[e], s[i >> 1]);
+              *reinterpret_cast<uint4*>(dst + r * 128 + ((((c & 1) * 4 + i) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&rawfree[rs]);
+            mbar_arrive(&full[st]);
+          }
+          if (++rs == NRAW) {
+            rs = 0;
+            rph ^= 1u;
+          }
+          if (++st == NST) {
+            st = 0;
+            sph ^= 1u;
+          }
+        }
+      }
+    }
   } else if (warp < 8) {   // (one-tile items leave warp 10 idle)
     // ------------------------------------------------- softmax and epilogue
     const int s = warp >> 2;                        // group
@@ -925,7 +1024,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
       const int tok = it.tok0 + (TWO ? s * p.tile_toks : 0) + t;   // of the request
       const bool live = t < p.tile_toks && tok < it.n;
       float scale = p.scale_log2;
-      if constexpr (FP8) {
+      if constexpr (CODES) {
         // Q row -> f16, scaled by a power of two that brings its largest
         // magnitude to [2^14, 2^15).  Where both groups read one tile, both
         // look at the whole row, then convert a half each.  (Loops kept short:
@@ -937,8 +1036,8 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           uint8_t* row = qbase + slot * TILE + r * 128;
           float amax = 0.f;
 #pragma unroll 2
-          for (int c = 0; c < 16; ++c) {
-            const uint4 v = *reinterpret_cast<const uint4*>(row + (c >> 3) * (TILE / 2) + (((c & 7) ^ (r & 7)) << 4));
+          for (int c = 0; c < D / 8; ++c) {
+            const uint4 v = *reinterpret_cast<const uint4*>(row + (c >> 3) * (TILE / HB) + (((c & 7) ^ (r & 7)) << 4));
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k)
@@ -950,9 +1049,9 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           scale *= __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
           if (!TWO) named_barrier(1, 256);
 #pragma unroll 1
-          for (int c0 = 0; c0 < (TWO ? 16 : 8); ++c0) {
-            const int c = TWO ? c0 : s * 8 + c0;
-            uint4* q4 = reinterpret_cast<uint4*>(row + (c >> 3) * (TILE / 2) + (((c & 7) ^ (r & 7)) << 4));
+          for (int c0 = 0; c0 < (TWO ? D / 8 : D / 16); ++c0) {
+            const int c = TWO ? c0 : s * (D / 16) + c0;
+            uint4* q4 = reinterpret_cast<uint4*>(row + (c >> 3) * (TILE / HB) + (((c & 7) ^ (r & 7)) << 4));
             const uint4 v = *q4;
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
             uint32_t o[4];
@@ -966,7 +1065,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           if (lane == 0) mbar_arrive(&qconv[slot]);
         }
       }
-      constexpr float LIFT = FP8 ? kRowsLiftF16 : 0.f;
+      constexpr float LIFT = CODES ? kRowsLiftF16 : 0.f;
       const float lazy = kRowsLazy / scale;
       const int bound = live ? ctx + tok : -1;      // causal: its last position
       // first position that some row of the tile does not see
@@ -997,7 +1096,7 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
         // their exponentials (128 scores in registers spill, and that costs more)
         uint32_t x[2][32];
         float top = -INFINITY;
-#pragma unroll (FP8 && TWO ? 1 : 2)   // (rolled: 4 chunks of 1600 tokens over E4M3 583 against 595 us, over bf16 477 against 472)
+#pragma unroll (CODES && TWO ? 1 : 2)   // (rolled: 4 chunks of 1600 tokens over E4M3 583 against 595 us, over bf16 477 against 472)
         for (int half = 1; half >= 0; --half) {
           tmem_ld32_async(ts + 64 * half, x[0]);
           tmem_ld32_async(ts + 64 * half + 32, x[1]);
@@ -1037,8 +1136,8 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&pfull[2 * s + h]);
         };
-        row_exp<FP8>(ts, 0, x[0], scale, negm, sum[0]);
-        row_exp<FP8>(ts, 1, x[1], scale, negm, sum[1]);
+        row_exp<CODES>(ts, 0, x[0], scale, negm, sum[0]);
+        row_exp<CODES>(ts, 1, x[1], scale, negm, sum[1]);
         tmem_ld32_async(ts + 64, x[0]);
         tmem_ld32_async(ts + 96, x[1]);
         hand_over(0);
@@ -1048,8 +1147,8 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
           row_mask(w[2], x[0]);
           row_mask(w[3], x[1]);
         }
-        row_exp<FP8>(ts, 2, x[0], scale, negm, sum[0]);
-        row_exp<FP8>(ts, 3, x[1], scale, negm, sum[1]);
+        row_exp<CODES>(ts, 2, x[0], scale, negm, sum[0]);
+        row_exp<CODES>(ts, 3, x[1], scale, negm, sum[1]);
         hand_over(1);
         l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
       }
@@ -1167,22 +1266,22 @@ __global__ void __launch_bounds__(FP8 ? 512 : 384, 1)
   }
 }
 
-template <int D, bool FP8, bool TWO, bool LANES>
+template <int D, int KV, bool TWO, bool LANES>
 cudaError_t launch_rows_attn_one(const CUtensorMap& kv_map, const CUtensorMap& q_map, const RowsAttnParams& p,
                                  size_t smem, cudaStream_t st) {
-  const void* fn = reinterpret_cast<const void*>(&rows_attn_kernel<D, FP8, TWO, LANES>);
+  const void* fn = reinterpret_cast<const void*>(&rows_attn_kernel<D, KV, TWO, LANES>);
   const cudaError_t e = ensure_smem_attr(fn, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(rows_attn_kernel<D, FP8, TWO, LANES>, dim3(p.num_ctas), dim3(FP8 ? 512 : 384), smem, st, kv_map, q_map, p);
+  return launch_pdl(rows_attn_kernel<D, KV, TWO, LANES>, dim3(p.num_ctas), dim3(KV != TRTV_BF16 ? 512 : 384), smem, st, kv_map, q_map, p);
 }
 
 // two: 256-row items, in `items` lanes where a tree has more than one a head
-template <int D, bool FP8>
+template <int D, int KV>
 cudaError_t launch_rows_attn_kind(bool two, const CUtensorMap& kv_map, const CUtensorMap& q_map, const RowsAttnParams& p,
                                   size_t smem, cudaStream_t st) {
-  if (!two) return launch_rows_attn_one<D, FP8, false, false>(kv_map, q_map, p, smem, st);
-  return p.items > 1 ? launch_rows_attn_one<D, FP8, true, true>(kv_map, q_map, p, smem, st)
-                     : launch_rows_attn_one<D, FP8, true, false>(kv_map, q_map, p, smem, st);
+  if (!two) return launch_rows_attn_one<D, KV, false, false>(kv_map, q_map, p, smem, st);
+  return p.items > 1 ? launch_rows_attn_one<D, KV, true, true>(kv_map, q_map, p, smem, st)
+                     : launch_rows_attn_one<D, KV, true, false>(kv_map, q_map, p, smem, st);
 }
 
 }  // namespace trtv

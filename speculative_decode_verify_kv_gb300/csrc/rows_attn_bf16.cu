@@ -6,8 +6,8 @@ namespace trtv {
 
 cudaError_t launch_rows_attn_bf16(int head_dim, bool two, const CUtensorMap& kv_map, const CUtensorMap& q_map,
                                   const RowsAttnParams& p, size_t smem, cudaStream_t st) {
-  return head_dim == 64 ? launch_rows_attn_kind<64, false>(two, kv_map, q_map, p, smem, st)
-                        : launch_rows_attn_kind<128, false>(two, kv_map, q_map, p, smem, st);
+  return head_dim == 64 ? launch_rows_attn_kind<64, TRTV_BF16>(two, kv_map, q_map, p, smem, st)
+                        : launch_rows_attn_kind<128, TRTV_BF16>(two, kv_map, q_map, p, smem, st);
 }
 
 }  // namespace trtv

@@ -7,7 +7,7 @@ namespace trtv {
 
 cudaError_t launch_rows_attn_fp8(bool two, const CUtensorMap& kv_map, const CUtensorMap& q_map,
                                  const RowsAttnParams& p, size_t smem, cudaStream_t st) {
-  return launch_rows_attn_kind<128, true>(two, kv_map, q_map, p, smem, st);
+  return launch_rows_attn_kind<128, TRTV_FP8_E4M3>(two, kv_map, q_map, p, smem, st);
 }
 
 // Joins the pieces o_i (each normalised by its own sum, log2 lse_i) of a cut

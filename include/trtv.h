@@ -96,6 +96,9 @@ typedef enum { TRTV_BF16 = 0, TRTV_FP8_E4M3 = 1, TRTV_F32 = 2, TRTV_FP4_E2M1 = 3
 #define TRTV_DEVERR_POSITION 32 /* a token's rotary position outside [0, table_len) */
 #define TRTV_DEVERR_PATH 64     /* an accepted path that is not strictly ascending, leaves its tree
                                    or is longer than it */
+#define TRTV_DEVERR_SLOTS 128   /* a fork that needs more slots than are free */
+#define TRTV_DEVERR_REFS 256    /* a negative reference count, or a page held that has none */
+#define TRTV_DEVERR_PARENT 512  /* a parent outside [-1, batch) */
 
 typedef struct {
   int32_t batch;             /* requests B >= 1 */
@@ -510,6 +513,82 @@ trtv_status trtv_tree_commit(const trtv_geom* geom, void* kv_pool, const int32_t
                              const int32_t* kv_lens, const int32_t* qo_indptr,
                              const int32_t* path, const int32_t* path_len, int32_t max_path,
                              int32_t* new_kv_lens, void* stream);
+
+/*
+ * ---- Pages under the tables ------------------------------------------------
+ * The calls below manage the slots of a pool on the device.  A slot's reference
+ * count is the number of requests that hold it (and of other holders, a prefix
+ * cache say), 0 when it is free; nothing else is kept.
+ *   ref_count  int32 [num_slots]
+ *   num_pages  int32 [batch]: request b holds the slots page_table[b][0 ..
+ *              num_pages[b]): those of its length, and any room behind it
+ *   buffers    page buffers of a slot that are copied with it, from the slot's
+ *              first, 1 .. slot_stride (2: this layer's K and V; slot_stride: all)
+ * The geometry is the attention calls' (batch <= 2048, any cache type; qo_len,
+ * the query heads and the scales are checked but not used).  Whatever the GPU
+ * does first, the same inputs give the same slots.  All errors in the data are
+ * found before anything is changed: the device error word is set, new_ref_count
+ * gets ref_count's values and no other output is written.  Calls must be ordered
+ * with whatever else uses the pool.
+ */
+
+/* Workspace bytes of both calls (new_batch: of a fork, 0 to compact); 0 on a
+ * geometry or new_batch that they refuse.  256-byte aligned, no initial contents
+ * required; calls that may overlap must not share one. */
+size_t trtv_workspace_bytes_pages(const trtv_geom* geom, int32_t new_batch);
+
+/*
+ * The next step's requests from this one's: new request c goes on from request
+ * parent[c] (beams and samples: several from one; reordering a batch), or starts
+ * empty (parent -1), and gets room for new_tokens[c] more tokens.  A request that
+ * is no new one's parent ends, and what nobody holds any more is free.  With
+ * L = kv_lens[parent[c]] (0 for -1):
+ *   new_kv_lens[c] = L + new_tokens[c],  new_num_pages[c] = ceil(new_kv_lens[c] / 128).
+ *   The L / 128 full pages are shared: the slots of the parent.
+ *   Pages behind them are written to, so nobody shares them.  The first new
+ *   request of a parent (the smallest c) keeps the parent's, from page L / 128 on
+ *   as long as it holds them alone (ref_count 1); every other such page is a
+ *   fresh slot, and page L / 128 then gets a copy of the parent's L % 128 rows.
+ *   Fresh slots are the free ones (ref_count 0 before the call) in ascending
+ *   order, handed out in order of c and page.
+ *   new_ref_count: what the old batch held is given back, what the new one holds
+ *   is counted.  Pages beyond ceil(new_kv_lens / 128) are given back too.
+ *   ref_count     (read)
+ *   kv_lens       int32 [batch], 0 <= kv_lens <= 128 * max_pages_per_req (read)
+ *   num_pages     (read) or NULL: ceil(kv_lens / 128)
+ *   parent        int32 [new_batch] (read), 1 <= new_batch <= 2048
+ *   new_tokens    int32 [new_batch], >= 0 (read), or NULL: none
+ *   new_ref_count int32 [num_slots] (written), may be ref_count itself
+ *   new_page_table int32 [new_batch, max_pages_per_req] (written, 0 behind a
+ *                 request's pages), new_kv_lens, new_num_pages int32 [new_batch]
+ *                 (written; new_num_pages may be NULL): not the old ones
+ * Errors in the data: TRTV_DEVERR_KV_LEN (a length, num_pages or new_tokens that
+ * does not fit), _PAGE_ID, _REFS, _PARENT, _SLOTS (more fresh slots than free ones).
+ */
+trtv_status trtv_pages_fork(const trtv_geom* geom, void* kv_pool, int32_t buffers, const int32_t* ref_count,
+                            const int32_t* page_table, const int32_t* kv_lens, const int32_t* num_pages,
+                            const int32_t* parent, const int32_t* new_tokens, int32_t new_batch,
+                            int32_t* new_ref_count, int32_t* new_page_table, int32_t* new_kv_lens,
+                            int32_t* new_num_pages, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * The used slots to the front of the pool: with U used slots, those from slot U
+ * on move, in ascending order, to the free slots below U, in ascending order;
+ * the others stay.  Whole pages are copied.
+ *   num_pages     (read, not NULL), 0 <= num_pages <= max_pages_per_req
+ *   slot_map      int32 [num_slots] (written): where each slot went, -1 for a free
+ *                 one (other holders follow it)
+ *   num_used      int32 [1] (written): U
+ *   new_ref_count int32 [num_slots] (written), may be ref_count itself
+ *   new_page_table int32 [batch, max_pages_per_req] (written, 0 behind a
+ *                 request's pages), may be page_table itself
+ * Errors in the data: TRTV_DEVERR_KV_LEN (a num_pages that does not fit), _PAGE_ID,
+ * _REFS.
+ */
+trtv_status trtv_pages_compact(const trtv_geom* geom, void* kv_pool, int32_t buffers, const int32_t* ref_count,
+                               const int32_t* page_table, const int32_t* num_pages, int32_t* slot_map,
+                               int32_t* num_used, int32_t* new_ref_count, int32_t* new_page_table,
+                               void* workspace, size_t ws_bytes, void* stream);
 
 /*
  * Test hook for the bounded waits (the CUDA-graphs commit of "Eagle3 for M3

@@ -23,13 +23,15 @@ __all__ = [
     "trtv_page_table_from_flat", "trtv_workspace_bytes_flat", "trtv_verify_dense_flat",
     "trtv_draft_attn_p32", "trtv_msa_select", "trtv_msa_verify", "trtv_status_string",
     "trtv_test_withhold_pages", "trtv_norm_rope_stage", "trtv_workspace_bytes_rows", "trtv_prompt_attn",
-    "trtv_verify_tree", "trtv_tree_commit", "trtv_read_kv", "NormRope", "geom_of", "EXPORTS",
+    "trtv_verify_tree", "trtv_tree_commit", "trtv_read_kv", "trtv_workspace_bytes_pages",
+    "trtv_pages_fork", "trtv_pages_compact", "NormRope", "geom_of", "EXPORTS",
 ]
 
 TRTV_OK, TRTV_ERR_INVALID_ARG, TRTV_ERR_UNSUPPORTED, TRTV_ERR_CUDA, TRTV_ERR_WORKSPACE = range(5)
 TRTV_BF16, TRTV_FP8_E4M3, TRTV_F32, TRTV_FP4_E2M1 = 0, 1, 2, 3
 DEVERR_KV_LEN, DEVERR_PAGE_ID, DEVERR_BLOCK_IDX, DEVERR_TIMEOUT = 1, 2, 4, 8
 DEVERR_INDPTR, DEVERR_POSITION, DEVERR_PATH = 16, 32, 64
+DEVERR_SLOTS, DEVERR_REFS, DEVERR_PARENT = 128, 256, 512
 
 # every function the C header declares
 EXPORTS = ("trtv_status_string", "trtv_version", "trtv_subpage_view", "trtv_workspace_bytes",
@@ -38,7 +40,8 @@ EXPORTS = ("trtv_status_string", "trtv_version", "trtv_subpage_view", "trtv_work
            "trtv_page_table_from_flat", "trtv_workspace_bytes_flat", "trtv_verify_dense_flat",
            "trtv_draft_attn_p32", "trtv_msa_select", "trtv_msa_verify", "trtv_test_withhold_pages",
            "trtv_get_device_error", "trtv_norm_rope_stage", "trtv_workspace_bytes_rows", "trtv_prompt_attn",
-           "trtv_verify_tree", "trtv_tree_commit", "trtv_read_kv")
+           "trtv_verify_tree", "trtv_tree_commit", "trtv_read_kv", "trtv_workspace_bytes_pages", "trtv_pages_fork",
+           "trtv_pages_compact")
 
 
 class TrtvError(RuntimeError):
@@ -138,6 +141,12 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     h.trtv_tree_commit.argtypes = [G, vp, vp, vp, vp, vp, vp, i32, vp, vp]
     h.trtv_read_kv.restype = ctypes.c_int
     h.trtv_read_kv.argtypes = [G, vp, vp, vp, vp, i32, vp, vp, vp]
+    h.trtv_workspace_bytes_pages.restype = sz
+    h.trtv_workspace_bytes_pages.argtypes = [G, i32]
+    h.trtv_pages_fork.restype = ctypes.c_int
+    h.trtv_pages_fork.argtypes = [G, vp, i32, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, vp, vp, sz, vp]
+    h.trtv_pages_compact.restype = ctypes.c_int
+    h.trtv_pages_compact.argtypes = [G, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     _lib = h
     return h
 
@@ -401,6 +410,14 @@ def trtv_workspace_bytes_rows(geom: Geom) -> int:
     return load().trtv_workspace_bytes_rows(ctypes.byref(geom))
 
 
+def _workspace_arg(fn: str, workspace, ws_bytes: int, dev: int) -> int:
+    if workspace.__class__ is int:
+        return workspace
+    if workspace.get_device() != dev or workspace.nbytes < ws_bytes or not workspace.is_contiguous():
+        _refuse(fn, "workspace", workspace, dev, "any type,", (f"{ws_bytes} bytes",))
+    return workspace.data_ptr()
+
+
 def _rows_attn(fn: str, geom: Geom, q, kv_pool, page_table, kv_lens, qo_indptr, tree_mask, out, out_dtype: int,
                workspace, ws_bytes: int, stream) -> None:
     dev, st = _begin(stream)
@@ -415,11 +432,7 @@ def _rows_attn(fn: str, geom: Geom, q, kv_pool, page_table, kv_lens, qo_indptr, 
                          uint32 if uint32 is not None and getattr(tree_mask, "dtype", None) is uint32 else _torch.int32,
                          (rows, (geom.qo_len + 31) // 32)))
     args.append(_arg(fn, "out", out, dev, _torch.float32 if out_dtype == TRTV_F32 else _torch.bfloat16, shape))
-    if workspace.__class__ is not int:
-        if workspace.get_device() != dev or workspace.nbytes < ws_bytes or not workspace.is_contiguous():
-            _refuse(fn, "workspace", workspace, dev, "any type,", (f"{ws_bytes} bytes",))
-        workspace = workspace.data_ptr()
-    _check(fn, getattr(load(), fn)(*args, out_dtype, workspace, ws_bytes, st))
+    _check(fn, getattr(load(), fn)(*args, out_dtype, _workspace_arg(fn, workspace, ws_bytes, dev), ws_bytes, st))
 
 
 def trtv_prompt_attn(geom: Geom, q, kv_pool, page_table, kv_lens, qo_indptr, out, out_dtype: int, workspace,
@@ -462,3 +475,43 @@ def trtv_read_kv(geom: Geom, kv_pool, page_table, kv_lens, qo_indptr, k_out, v_o
     _check(fn, load().trtv_read_kv(ctypes.byref(geom), _pool_arg(fn, geom, kv_pool, dev), pt, kl, ip, rows,
                                    0 if k_out is None else _arg(fn, "k_out", k_out, dev, _torch.bfloat16, shape),
                                    0 if v_out is None else _arg(fn, "v_out", v_out, dev, _torch.bfloat16, shape), st))
+
+
+# -- pages under the tables ----------------------------------------------------
+
+def trtv_workspace_bytes_pages(geom: Geom, new_batch: int = 0) -> int:
+    return load().trtv_workspace_bytes_pages(ctypes.byref(geom), new_batch)
+
+
+def trtv_pages_fork(geom: Geom, kv_pool, buffers: int, ref_count, page_table, kv_lens, num_pages, parent, new_tokens,
+                    new_ref_count, new_page_table, new_kv_lens, new_num_pages, workspace, ws_bytes: int, stream=None) -> None:
+    """The next step's requests from this one's: they share full pages, get copies of pages that they write to and
+    fresh slots for new_tokens more tokens (None: none); num_pages None: the pages of kv_lens."""
+    fn = "trtv_pages_fork"
+    dev, st = _begin(stream)
+    i32, b, mp, slots = _torch.int32, geom.batch, geom.max_pages_per_req, geom.num_slots
+    n = parent.shape[0]
+    _check(fn, load().trtv_pages_fork(
+        ctypes.byref(geom), _pool_arg(fn, geom, kv_pool, dev), buffers, _arg(fn, "ref_count", ref_count, dev, i32, (slots,)),
+        _arg(fn, "page_table", page_table, dev, i32, (b, mp)), _arg(fn, "kv_lens", kv_lens, dev, i32, (b,)),
+        0 if num_pages is None else _arg(fn, "num_pages", num_pages, dev, i32, (b,)),
+        _arg(fn, "parent", parent, dev, i32, (n,)),
+        0 if new_tokens is None else _arg(fn, "new_tokens", new_tokens, dev, i32, (n,)), n,
+        _arg(fn, "new_ref_count", new_ref_count, dev, i32, (slots,)),
+        _arg(fn, "new_page_table", new_page_table, dev, i32, (n, mp)), _arg(fn, "new_kv_lens", new_kv_lens, dev, i32, (n,)),
+        0 if new_num_pages is None else _arg(fn, "new_num_pages", new_num_pages, dev, i32, (n,)),
+        _workspace_arg(fn, workspace, ws_bytes, dev), ws_bytes, st))
+
+
+def trtv_pages_compact(geom: Geom, kv_pool, buffers: int, ref_count, page_table, num_pages, slot_map, num_used,
+                       new_ref_count, new_page_table, workspace, ws_bytes: int, stream=None) -> None:
+    """The used slots to the front of the pool; slot_map says where each went (-1: it was free)."""
+    fn = "trtv_pages_compact"
+    dev, st = _begin(stream)
+    i32, b, mp, slots = _torch.int32, geom.batch, geom.max_pages_per_req, geom.num_slots
+    _check(fn, load().trtv_pages_compact(
+        ctypes.byref(geom), _pool_arg(fn, geom, kv_pool, dev), buffers, _arg(fn, "ref_count", ref_count, dev, i32, (slots,)),
+        _arg(fn, "page_table", page_table, dev, i32, (b, mp)), _arg(fn, "num_pages", num_pages, dev, i32, (b,)),
+        _arg(fn, "slot_map", slot_map, dev, i32, (slots,)), _arg(fn, "num_used", num_used, dev, i32, (1,)),
+        _arg(fn, "new_ref_count", new_ref_count, dev, i32, (slots,)),
+        _arg(fn, "new_page_table", new_page_table, dev, i32, (b, mp)), _workspace_arg(fn, workspace, ws_bytes, dev), ws_bytes, st))

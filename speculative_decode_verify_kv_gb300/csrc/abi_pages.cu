@@ -1,0 +1,135 @@
+// abi_pages.cu -- the C ABI's page calls (include/trtv.h): forking and
+// compacting.  Host code only, as abi_rows.cu.
+#include "host.h"
+#include "launch.h"
+#include "pages.cuh"
+
+namespace trtv {
+namespace {
+
+constexpr int kMaxNew = 2048;   // new requests: their sums lie in shared memory
+
+struct PagesPlan {
+  int chunks;
+  size_t free, list, rank, bad, children, kept, child, total;
+};
+
+PagesPlan pages_plan(const trtv_geom* g, int new_batch) {
+  PagesPlan pl;
+  const size_t slots = static_cast<size_t>(g->num_slots), batch = static_cast<size_t>(g->batch), N = static_cast<size_t>(new_batch);
+  pl.chunks = static_cast<int>((slots + kSlotChunk - 1) / kSlotChunk);
+  size_t off = 0;
+  auto take = [&](size_t n) {
+    const size_t at = off;
+    off = align_up(off + n, 256);
+    return at;
+  };
+  pl.free = take(pl.chunks * sizeof(int));
+  pl.list = take(static_cast<size_t>(pl.chunks) * kSlotChunk * sizeof(int));
+  pl.rank = take(slots * sizeof(int));
+  pl.bad = take((pl.chunks + batch + N) * sizeof(int));
+  pl.children = take(batch * sizeof(int));
+  pl.kept = take(batch * sizeof(int));
+  pl.child = take(N * sizeof(int2));
+  pl.total = off;
+  return pl;
+}
+
+// What both calls check and set up.
+trtv_status pages_common(const trtv_geom* g, void* pool, int32_t buffers, const int32_t* ref, const int32_t* page_table,
+                         const int32_t* num_pages, int32_t* new_ref, int32_t* new_table, int new_batch, void* ws,
+                         size_t ws_bytes, PagesParams* p) {
+  const int32_t any = 0;   // (no rows: a host pointer that nothing reads)
+  trtv_status s = rows_geometry(g, &any, 0, &p->g);
+  if (s != TRTV_OK) return s;
+  if (pool == nullptr || ref == nullptr || page_table == nullptr || new_ref == nullptr || new_table == nullptr)
+    return TRTV_ERR_INVALID_ARG;
+  if (!aligned(pool, 16) || !aligned(ref, 4) || !aligned(page_table, 4) || !aligned(num_pages, 4) || !aligned(new_ref, 4) ||
+      !aligned(new_table, 4))
+    return TRTV_ERR_INVALID_ARG;
+  if (buffers < 1 || buffers > g->slot_stride) return TRTV_ERR_INVALID_ARG;
+  const PagesPlan pl = pages_plan(g, new_batch);
+  if (ws == nullptr || !aligned(ws, 256) || ws_bytes < pl.total) return TRTV_ERR_WORKSPACE;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  p->ws.free = reinterpret_cast<int*>(w + pl.free);
+  p->ws.list = reinterpret_cast<int*>(w + pl.list);
+  p->ws.rank = reinterpret_cast<int*>(w + pl.rank);
+  p->ws.bad = reinterpret_cast<int*>(w + pl.bad);
+  p->ws.children = reinterpret_cast<int*>(w + pl.children);
+  p->ws.kept = reinterpret_cast<int*>(w + pl.kept);
+  p->ws.child = reinterpret_cast<int2*>(w + pl.child);
+  p->chunks = pl.chunks;
+  p->pool = static_cast<uint8_t*>(pool);
+  p->ref = ref;
+  p->num_pages = num_pages;
+  p->new_ref = new_ref;
+  p->new_table = new_table;
+  p->new_batch = new_batch;
+  p->buffers = buffers;
+  p->row_bytes = g->kv_dtype == TRTV_FP4_E2M1 ? 0 : g->head_dim * (g->kv_dtype == TRTV_FP8_E4M3 ? 1 : 2);
+  p->block_bytes = g->kv_dtype == TRTV_FP4_E2M1 ? kFp4Row * g->head_dim : kSub * p->row_bytes;
+  p->g.page_table = page_table;
+  return TRTV_OK;
+}
+
+}  // namespace
+}  // namespace trtv
+
+using namespace trtv;
+
+extern "C" {
+
+size_t trtv_workspace_bytes_pages(const trtv_geom* geom, int32_t new_batch) {
+  RowsGeom r{};
+  const int32_t any = 0;
+  if (rows_geometry(geom, &any, 0, &r) != TRTV_OK || new_batch < 0 || new_batch > kMaxNew) return 0;
+  return pages_plan(geom, new_batch).total;
+}
+
+trtv_status trtv_pages_fork(const trtv_geom* g, void* kv_pool, int32_t buffers, const int32_t* ref_count,
+                            const int32_t* page_table, const int32_t* kv_lens, const int32_t* num_pages,
+                            const int32_t* parent, const int32_t* new_tokens, int32_t new_batch, int32_t* new_ref_count,
+                            int32_t* new_page_table, int32_t* new_kv_lens, int32_t* new_num_pages, void* workspace,
+                            size_t ws_bytes, void* stream) {
+  if (new_batch < 1) return TRTV_ERR_INVALID_ARG;
+  if (new_batch > kMaxNew) return TRTV_ERR_UNSUPPORTED;
+  PagesParams p{};
+  trtv_status s = pages_common(g, kv_pool, buffers, ref_count, page_table, num_pages, new_ref_count, new_page_table, new_batch,
+                               workspace, ws_bytes, &p);
+  if (s != TRTV_OK) return s;
+  if (kv_lens == nullptr || parent == nullptr || new_kv_lens == nullptr || !aligned(kv_lens, 4) || !aligned(parent, 4) ||
+      !aligned(new_tokens, 4) || !aligned(new_kv_lens, 4) || !aligned(new_num_pages, 4))
+    return TRTV_ERR_INVALID_ARG;
+  // a request may come from any old one: the old tables and lengths are read while the new are written
+  if (new_page_table == page_table || new_kv_lens == kv_lens || (num_pages != nullptr && new_num_pages == num_pages))
+    return TRTV_ERR_INVALID_ARG;
+  const int sms = sm_count();
+  p.g.err = err_word();
+  if (sms <= 0 || p.g.err == nullptr) return TRTV_ERR_CUDA;
+  p.g.kv_lens = kv_lens;
+  p.parent = parent;
+  p.new_tokens = new_tokens;
+  p.new_lens = new_kv_lens;
+  p.new_num_pages = new_num_pages;
+  return launch_pages_fork(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TRTV_OK : TRTV_ERR_CUDA;
+}
+
+trtv_status trtv_pages_compact(const trtv_geom* g, void* kv_pool, int32_t buffers, const int32_t* ref_count,
+                               const int32_t* page_table, const int32_t* num_pages, int32_t* slot_map, int32_t* num_used,
+                               int32_t* new_ref_count, int32_t* new_page_table, void* workspace, size_t ws_bytes,
+                               void* stream) {
+  PagesParams p{};
+  trtv_status s = pages_common(g, kv_pool, buffers, ref_count, page_table, num_pages, new_ref_count, new_page_table, 0, workspace,
+                               ws_bytes, &p);
+  if (s != TRTV_OK) return s;
+  if (num_pages == nullptr || slot_map == nullptr || num_used == nullptr || !aligned(slot_map, 4) || !aligned(num_used, 4))
+    return TRTV_ERR_INVALID_ARG;
+  const int sms = sm_count();
+  p.g.err = err_word();
+  if (sms <= 0 || p.g.err == nullptr) return TRTV_ERR_CUDA;
+  p.slot_map = slot_map;
+  p.num_used = num_used;
+  return launch_pages_compact(p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TRTV_OK : TRTV_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -227,6 +227,10 @@ trtv_status rows_attn(const trtv_geom* g, const void* q, const void* pool, const
 
 }  // namespace
 
+trtv_status rows_geometry(const trtv_geom* g, const int32_t* indptr, int32_t num_tokens, RowsGeom* r) {
+  return rows_geom(g, indptr, num_tokens, r);
+}
+
 // The ladder over an E2M1 cache: the packed-row call with qo_len rows per request.
 constexpr int kMaxLadder = 32;
 trtv_status ladder_fp4(const trtv_geom* g, const void* q, const void* pool, const int32_t* page_table,

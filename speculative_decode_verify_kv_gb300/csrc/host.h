@@ -19,6 +19,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder();  // null when the driver has none
 uint64_t wait_limit_ns();                     // bounded-wait settings of the next launches
 int withheld_pages();
 
+struct RowsGeom;
+// Geometry checks of the packed-row and page calls (abi_rows.cu).
+trtv_status rows_geometry(const trtv_geom* g, const int32_t* indptr, int32_t num_tokens, RowsGeom* r);
+
 // Dense ladder attention over an E2M1 cache (abi_rows.cu); g is not null.
 trtv_status ladder_fp4(const trtv_geom* g, const void* q, const void* pool, const int32_t* page_table,
                        const int32_t* kv_lens, void* out, int32_t out_dtype, void* ws, size_t ws_bytes, void* stream);

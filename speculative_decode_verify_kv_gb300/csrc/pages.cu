@@ -1,0 +1,446 @@
+// pages.cu -- forking, growing and freeing requests over shared pages, and
+// compacting a pool, on the device.
+//
+// The only state of the slots is their reference counts (0: free).  Two kernels
+// a call:
+//   pages_scan_kernel     a CTA per 1024 slots lists the free ones and the used
+//                         ones; a warp per request checks what it holds and, of
+//                         a new request, counts the fresh slots that it needs
+//   pages_fork_kernel     every CTA sums up the counts (a few hundred integers,
+//   pages_compact_kernel  cheaper than another launch), so that the k-th free
+//                         slot of the pool is a search in the sums and one load;
+//                         then tables, reference counts and page bytes, spread
+//                         over all CTAs
+// Which slots are taken depends on the counts alone, never on timing: reference
+// counts change by integer atomics, and every other word has one writer.  An
+// error found by the first kernel keeps the second from writing anything.
+#include "launch.h"
+#include "pages.cuh"
+
+namespace trtv {
+namespace {
+
+// ceil(tokens / 128) for tokens >= 0
+__device__ __forceinline__ int pages_for(int64_t tokens) { return static_cast<int>((tokens + kPage - 1) / kPage); }
+
+// What request a holds: its length and pages; ok = false for lengths that fit
+// neither the table nor the pages.
+struct Held {
+  int len, pages;
+  bool ok;
+};
+__device__ __forceinline__ Held held_by(const PagesParams& p, int a) {
+  if (p.g.kv_lens == nullptr) {   // compacting: the pages alone
+    const int n = p.num_pages[a];
+    return n < 0 || n > p.g.max_pages ? Held{0, 0, false} : Held{0, n, true};
+  }
+  const int len = p.g.kv_lens[a];
+  if (!len_valid(len, 0, p.g.max_pages)) return {0, 0, false};
+  const int least = pages_for(len), n = p.num_pages != nullptr ? p.num_pages[a] : least;
+  if (n < least || n > p.g.max_pages) return {0, 0, false};
+  return {len, n, true};
+}
+
+// Sum over the CTA's threads before this one, and of all of them; `tot` has 8 words.
+template <typename I>
+__device__ __forceinline__ I block_before(I x, I* tot, I& all) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  I incl = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const I v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  __syncthreads();   // (tot may still be read from before)
+  if (lane == 31) tot[warp] = incl;
+  __syncthreads();
+  I before = incl - x;
+  all = 0;
+#pragma unroll
+  for (int w = 0; w < kPagesThreads / 32; ++w) {
+    if (w < warp) before += tot[w];
+    all += tot[w];
+  }
+  return before;
+}
+
+// Exclusive sums of n counts into pre[0 .. n], capped so that they cannot pass 2^30.
+template <typename F>
+__device__ __forceinline__ int block_sums(int n, int* pre, int64_t* tot, F count) {
+  constexpr int64_t kCap = 1 << 30;
+  int64_t run = 0;
+  for (int i0 = 0; i0 < n; i0 += kPagesThreads) {
+    const int i = i0 + threadIdx.x;
+    int64_t all;
+    const int64_t before = block_before(static_cast<int64_t>(i < n ? count(i) : 0), tot, all);
+    if (i < n) pre[i] = static_cast<int>(min(kCap, run + before));
+    run += all;
+  }
+  run = min(kCap, run);
+  if (threadIdx.x == 0) pre[n] = static_cast<int>(run);
+  __syncthreads();
+  return static_cast<int>(run);
+}
+
+// The largest i in [0, n) with pre[i] <= k: k lies in its share when k < pre[n]
+// (shares may be empty).
+__device__ __forceinline__ int share_of(const int* pre, int n, int k) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pre[mid] <= k) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ void copy16(uint8_t* dst, const uint8_t* src, int bytes, int lane) {
+  const uint4* s = reinterpret_cast<const uint4*>(src);
+  uint4* d = reinterpret_cast<uint4*>(dst);
+  const int n = bytes / 16;
+  constexpr int kFlight = 8;
+  for (int i = lane; i < n; i += 32 * kFlight) {
+    uint4 v[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u)
+      if (i + 32 * u < n) v[u] = s[i + 32 * u];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u)
+      if (i + 32 * u < n) d[i + 32 * u] = v[u];
+  }
+}
+
+}  // namespace
+
+template <bool COMPACT>
+__global__ void __launch_bounds__(kPagesThreads) pages_scan_kernel(const __grid_constant__ PagesParams p) {
+  __shared__ int tot[kPagesThreads / 32];
+  const RowsGeom& g = p.g;
+  const int tid = threadIdx.x, lane = tid & 31;
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x < p.chunks) {
+    // ------------------------------------------------------------ 1024 slots
+    constexpr int PER = kSlotChunk / kPagesThreads;
+    const int base = blockIdx.x * kSlotChunk, s0 = base + tid * PER;
+    int ref[PER], nfree = 0, nused = 0;
+    bool neg = false;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const bool in = s0 + i < g.num_slots;
+      ref[i] = in ? p.ref[s0 + i] : 0;
+      neg |= ref[i] < 0;
+      nfree += in && ref[i] == 0;
+      nused += in && ref[i] != 0;
+    }
+    int free_all;
+    const int both = block_before(nfree | nused << 16, tot, free_all);   // (at most 1024 each)
+    free_all &= 0xffff;
+    int f = both & 0xffff, u = both >> 16;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int s = s0 + i;
+      if (s >= g.num_slots) continue;
+      p.new_ref[s] = ref[i];
+      if (ref[i] == 0) {
+        p.ws.list[base + f++] = s;
+      } else {
+        if (COMPACT) p.ws.rank[s] = u;
+        p.ws.list[base + free_all + u++] = s;
+      }
+    }
+    const bool bad = __syncthreads_or(neg);
+    if (tid == 0) {
+      p.ws.free[blockIdx.x] = free_all;
+      p.ws.bad[blockIdx.x] = bad ? TRTV_DEVERR_REFS : 0;
+    }
+    return;
+  }
+  // ------------------------------------------------------------ a warp per request
+  const int unit = (blockIdx.x - p.chunks) * (kPagesThreads / 32) + (tid >> 5);
+  if (unit >= g.batch + p.new_batch) return;
+  int bad = 0;
+  if (unit < g.batch) {
+    // an old request: its pages, and how many new ones go on from it
+    const Held h = held_by(p, unit);
+    if (!h.ok) bad |= TRTV_DEVERR_KV_LEN;
+    const int32_t* row = g.page_table + static_cast<int64_t>(unit) * g.max_pages;
+#pragma unroll 4
+    for (int j = lane; j < h.pages; j += 32) {
+      const int s = row[j];
+      if (s < 0 || s >= g.num_slots) bad |= TRTV_DEVERR_PAGE_ID;
+      else if (p.ref[s] <= 0) bad |= TRTV_DEVERR_REFS;
+    }
+    if (!COMPACT) {
+      int n = 0;
+#pragma unroll 4
+      for (int c = lane; c < p.new_batch; c += 32) n += p.parent[c] == unit;
+      n = __reduce_add_sync(0xffffffffu, n);
+      if (lane == 0) p.ws.children[unit] = n;
+    }
+  } else if (!COMPACT) {
+    // a new request: the pages that it shares or keeps, and the fresh ones
+    const int c = unit - g.batch, a = p.parent[c], grow = p.new_tokens != nullptr ? p.new_tokens[c] : 0;
+    Held h{0, 0, true};
+    if (a < -1 || a >= g.batch) bad |= TRTV_DEVERR_PARENT;
+    else if (a >= 0) h = held_by(p, a);
+    const int64_t len = static_cast<int64_t>(h.len) + grow;
+    if (!h.ok || grow < 0 || len > static_cast<int64_t>(kPage) * g.max_pages) bad |= TRTV_DEVERR_KV_LEN;
+    if (bad == 0) {
+      const int full = h.len / kPage, need = pages_for(len);
+      int end = full;   // pages before the fresh ones
+      if (a >= 0) {
+        bool first = true;
+        for (int c0 = 0; c0 < c && first; c0 += 128) {
+          bool same = false;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int k = c0 + 32 * i + lane;
+            same |= k < c && p.parent[k] == a;
+          }
+          first = !__any_sync(0xffffffffu, same);
+        }
+        if (first) {
+          // the first new request of an old one keeps the pages to be written that nobody else holds
+          const int32_t* row = g.page_table + static_cast<int64_t>(a) * g.max_pages;
+          const int last = min(need, h.pages);
+          for (bool go = true; go && end < last;) {
+            const int j = end + lane;
+            const int s = j < last ? row[j] : -1;
+            const bool alone = s >= 0 && s < g.num_slots && p.ref[s] == 1;
+            const unsigned m = ~__ballot_sync(0xffffffffu, alone);
+            end += m == 0 ? 32 : __ffs(m) - 1;
+            go = m == 0;
+          }
+          if (lane == 0) p.ws.kept[a] = end;
+        }
+      }
+      if (lane == 0) p.ws.child[c] = make_int2(need - end, end);
+    } else if (lane == 0) {
+      p.ws.child[c] = make_int2(0, 0);
+    }
+  }
+  bad = __reduce_or_sync(0xffffffffu, bad);
+  if (lane == 0) p.ws.bad[p.chunks + unit] = bad;
+}
+
+// Shared memory of the second kernels: sums over the chunks, then (forking)
+// over the new requests' fresh slots and copied pages.
+size_t pages_smem(int chunks, int new_batch) { return (static_cast<size_t>(chunks) + 1 + 2 * (static_cast<size_t>(new_batch) + 1)) * sizeof(int); }
+
+namespace {
+
+// All bits that the scan found, for the whole CTA.
+__device__ __forceinline__ int found_bad(const PagesParams& p, int* word) {
+  if (threadIdx.x == 0) *word = 0;
+  __syncthreads();
+  int bad = 0;
+  for (int i = threadIdx.x; i < p.chunks + p.g.batch + p.new_batch; i += kPagesThreads) bad |= p.ws.bad[i];
+  if (bad != 0) atomicOr(word, bad);
+  __syncthreads();
+  return *word;
+}
+
+__device__ __forceinline__ int chunk_slots(const PagesParams& p, int i) { return min(kSlotChunk, p.g.num_slots - i * kSlotChunk); }
+
+}  // namespace
+
+// New tables, lengths and reference counts, and the copies of pages that are
+// written to.  A page is copied as far as it is live.
+__global__ void __launch_bounds__(kPagesThreads) pages_fork_kernel(const __grid_constant__ PagesParams p) {
+  extern __shared__ int sums[];
+  __shared__ int64_t tot[kPagesThreads / 32];
+  __shared__ int word;
+  const RowsGeom& g = p.g;
+  const int tid = threadIdx.x, lane = tid & 31, N = p.new_batch;
+  int* const slots = sums;                 // [chunks + 1] free slots before each chunk
+  int* const fresh = slots + p.chunks + 1; // [N + 1] fresh slots before each new request
+  int* const copies = fresh + N + 1;       // [N + 1] copied pages before it
+  pdl_wait();
+  pdl_trigger();
+  int bad = found_bad(p, &word);
+  if (bad == 0) {
+    const int have = block_sums(p.chunks, slots, tot, [&](int i) { return p.ws.free[i]; });
+    const int want = block_sums(N, fresh, tot, [&](int i) { return p.ws.child[i].x; });
+    if (want > have) bad = TRTV_DEVERR_SLOTS;
+  }
+  if (bad != 0) {
+    if (blockIdx.x == 0 && tid == 0) atomicOr(g.err, bad);
+    return;
+  }
+  auto parent_len = [&](int c) { return p.parent[c] >= 0 ? g.kv_lens[p.parent[c]] : 0; };
+  const int ncopies = block_sums(N, copies, tot, [&](int c) {
+    const int len = parent_len(c);
+    const int2 x = p.ws.child[c];
+    return x.x > 0 && x.y == len / kPage && len % kPage != 0 ? 1 : 0;
+  });
+  auto slot_of = [&](int k) {
+    const int i = share_of(slots, p.chunks, k);
+    return p.ws.list[i * kSlotChunk + k - slots[i]];
+  };
+
+  // ------------------------------------------------------------ tables
+  for (int c = blockIdx.x; c < N; c += gridDim.x) {
+    const int a = p.parent[c], len = parent_len(c), grow = p.new_tokens != nullptr ? p.new_tokens[c] : 0;
+    const int2 x = p.ws.child[c];
+    const int need = x.y + x.x;
+    const int32_t* from = g.page_table + static_cast<int64_t>(max(a, 0)) * g.max_pages;
+    int32_t* to = p.new_table + static_cast<int64_t>(c) * g.max_pages;
+    for (int j = tid; j < g.max_pages; j += kPagesThreads) {
+      int s = 0;
+      if (j < x.y) {
+        s = from[j];
+      } else if (j < need) {
+        s = slot_of(fresh[c] + j - x.y);
+        p.new_ref[s] = 1;
+      }
+      to[j] = s;
+    }
+    if (tid == 0) {
+      p.new_lens[c] = len + grow;
+      if (p.new_num_pages != nullptr) p.new_num_pages[c] = need;
+    }
+  }
+  // ------------------------------------------------------------ reference counts
+  for (int a = blockIdx.x; a < g.batch; a += gridDim.x) {
+    const Held h = held_by(p, a);
+    const int full = h.len / kPage, n = p.ws.children[a], kept = n > 0 ? p.ws.kept[a] : 0;
+    const int32_t* row = g.page_table + static_cast<int64_t>(a) * g.max_pages;
+    for (int j = tid; j < h.pages; j += kPagesThreads) {
+      const int change = (j < full ? n : j < kept ? 1 : 0) - 1;
+      if (change != 0 && atomicAdd(p.new_ref + row[j], change) + change < 0) atomicOr(g.err, TRTV_DEVERR_REFS);
+    }
+  }
+  // ------------------------------------------------------------ page bytes: a warp per 32 rows of a head
+  const int heads = g.num_kv_heads, per_copy = p.buffers * kGroups * heads;
+  const int64_t units = static_cast<int64_t>(ncopies) * per_copy;
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kPagesThreads / 32) + (tid >> 5); u < units;
+       u += static_cast<int64_t>(gridDim.x) * (kPagesThreads / 32)) {
+    const int k = static_cast<int>(u / per_copy), v = static_cast<int>(u % per_copy);
+    const int group = v / heads % kGroups;
+    const int c = share_of(copies, N, k), len = parent_len(c);
+    const int live = min(kSub, len % kPage - group * kSub);
+    if (live <= 0) continue;
+    const int64_t src = g.page_table[static_cast<int64_t>(p.parent[c]) * g.max_pages + len / kPage], dst = slot_of(fresh[c]);
+    const int64_t slot_blocks = static_cast<int64_t>(g.slot_stride) * kGroups * heads;
+    const uint8_t* s = p.pool + (src * slot_blocks + v) * p.block_bytes;
+    uint8_t* d = p.pool + (dst * slot_blocks + v) * p.block_bytes;
+    if (p.row_bytes != 0) {
+      copy16(d, s, live * p.row_bytes, lane);
+    } else {   // E2M1: D = block / 18; rows of D / 2 code bytes, then rows of D / 16 scales
+      const int D = p.block_bytes / kFp4Row, codes = kSub * D / 2;
+      copy16(d, s, live * (D / 2), lane);
+      for (int i = lane; i < live * (D / 64); i += 32)
+        reinterpret_cast<uint32_t*>(d + codes)[i] = reinterpret_cast<const uint32_t*>(s + codes)[i];
+    }
+  }
+}
+
+// With U used slots, the used slots from U on go to the free slots below U, in
+// ascending order of both: the j-th such free slot is the j-th free slot of the
+// pool, and the j-th such used slot the one with U - M used slots before it
+// plus j, M being their number.
+constexpr int kMoveBytes = 8192;   // that a warp copies at a time
+
+__global__ void __launch_bounds__(kPagesThreads) pages_compact_kernel(const __grid_constant__ PagesParams p) {
+  extern __shared__ int sums[];
+  __shared__ int64_t tot[kPagesThreads / 32];
+  __shared__ int word;
+  const RowsGeom& g = p.g;
+  const int tid = threadIdx.x, lane = tid & 31;
+  int* const slots = sums;   // [chunks + 1] free slots before each chunk
+  pdl_wait();
+  pdl_trigger();
+  const int bad = found_bad(p, &word);
+  if (bad != 0) {
+    if (blockIdx.x == 0 && tid == 0) atomicOr(g.err, bad);
+    return;
+  }
+  const int nfree = block_sums(p.chunks, slots, tot, [&](int i) { return p.ws.free[i]; });
+  const int U = g.num_slots - nfree;
+  // free slots below U: those of the chunks before U's, and some of its own
+  const int cu = U / kSlotChunk;
+  int64_t mine = 0, own;
+  if (cu < p.chunks) {
+    const int n = slots[cu + 1] - slots[cu];
+    for (int i = tid; i < n; i += kPagesThreads) mine += p.ws.list[cu * kSlotChunk + i] < U;
+  }
+  block_before(mine, tot, own);
+  const int M = (cu < p.chunks ? slots[cu] : nfree) + static_cast<int>(own), low = U - M;
+  auto used_before = [&](int i) { return min(i * kSlotChunk, g.num_slots) - slots[i]; };
+  auto free_slot = [&](int k) {
+    const int i = share_of(slots, p.chunks, k);
+    return p.ws.list[i * kSlotChunk + k - slots[i]];
+  };
+  auto used_slot = [&](int k) {
+    int lo = 0, hi = p.chunks;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (used_before(mid) <= k) lo = mid;
+      else hi = mid;
+    }
+    return p.ws.list[lo * kSlotChunk + (slots[lo + 1] - slots[lo]) + k - used_before(lo)];
+  };
+  if (blockIdx.x == 0 && tid == 0) *p.num_used = U;
+
+  // ------------------------------------------------------------ where every slot goes
+  for (int i = blockIdx.x; i < p.chunks; i += gridDim.x) {
+    const int n = chunk_slots(p, i), f = slots[i + 1] - slots[i];
+    for (int k = tid; k < n; k += kPagesThreads) {
+      const int s = p.ws.list[i * kSlotChunk + k];
+      int to = k < f ? -1 : s;
+      if (k >= f && s >= U) {
+        to = free_slot(used_before(i) + k - f - low);
+        p.new_ref[to] = p.ref[s];   // (the counts may be changed in place: one thread reads and clears s)
+        p.new_ref[s] = 0;
+      }
+      p.slot_map[s] = to;
+    }
+  }
+  // ------------------------------------------------------------ tables
+  for (int b = blockIdx.x; b < g.batch; b += gridDim.x) {
+    const int n = held_by(p, b).pages;
+    const int64_t row = static_cast<int64_t>(b) * g.max_pages;
+    for (int j = tid; j < g.max_pages; j += kPagesThreads) {
+      int s = 0;
+      if (j < n) {
+        s = g.page_table[row + j];
+        if (s >= U) s = free_slot(used_before(s / kSlotChunk) + p.ws.rank[s] - low);
+      }
+      p.new_table[row + j] = s;
+    }
+  }
+  // ------------------------------------------------------------ page bytes
+  const int64_t bytes = static_cast<int64_t>(p.buffers) * kGroups * g.num_kv_heads * p.block_bytes;   // side by side
+  const int64_t pitch = static_cast<int64_t>(g.slot_stride) * kGroups * g.num_kv_heads * p.block_bytes;
+  const int parts = static_cast<int>((bytes + kMoveBytes - 1) / kMoveBytes);
+  for (int64_t u = static_cast<int64_t>(blockIdx.x) * (kPagesThreads / 32) + (tid >> 5); u < static_cast<int64_t>(M) * parts;
+       u += static_cast<int64_t>(gridDim.x) * (kPagesThreads / 32)) {
+    const int j = static_cast<int>(u / parts);
+    const int64_t at = (u % parts) * kMoveBytes;
+    const int64_t src = used_slot(low + j), dst = free_slot(j);
+    copy16(p.pool + dst * pitch + at, p.pool + src * pitch + at, static_cast<int>(min(static_cast<int64_t>(kMoveBytes), bytes - at)), lane);
+  }
+}
+
+namespace {
+
+cudaError_t launch_two(bool compact, const PagesParams& p, int sms, cudaStream_t st) {
+  const size_t smem = pages_smem(p.chunks, p.new_batch);
+  const void* fn = compact ? reinterpret_cast<const void*>(&pages_compact_kernel) : reinterpret_cast<const void*>(&pages_fork_kernel);
+  cudaError_t e = ensure_smem_attr(fn, smem);
+  if (e != cudaSuccess) return e;
+  const int warps = kPagesThreads / 32, units = p.g.batch + p.new_batch;
+  const dim3 scan(static_cast<unsigned>(p.chunks + (units + warps - 1) / warps)), block(kPagesThreads);
+  e = launch_pdl(compact ? pages_scan_kernel<true> : pages_scan_kernel<false>, scan, block, 0, st, p);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(2 * sms));
+  return launch_pdl(compact ? pages_compact_kernel : pages_fork_kernel, grid, block, smem, st, p);
+}
+
+}  // namespace
+
+cudaError_t launch_pages_fork(const PagesParams& p, int sms, cudaStream_t st) { return launch_two(false, p, sms, st); }
+cudaError_t launch_pages_compact(const PagesParams& p, int sms, cudaStream_t st) { return launch_two(true, p, sms, st); }
+
+}  // namespace trtv

@@ -1,0 +1,46 @@
+// pages.cuh -- the pages under the page tables: launch parameters of forking and
+// compacting.
+#pragma once
+
+#include "rows.cuh"
+
+namespace trtv {
+
+constexpr int kSlotChunk = 1024;      // slots that one CTA of the scan takes
+constexpr int kPagesThreads = 256;
+
+// Workspace of both calls.
+struct PagesWs {
+  int* free;      // [chunks] free slots of each chunk
+  int* list;      // [chunks * kSlotChunk] a chunk's free slots, ascending, then its used slots, ascending
+  int* rank;      // [num_slots] compacting: a used slot's place among its chunk's used slots
+  int* bad;       // [chunks + batch + new_batch] TRTV_DEVERR_* bits that each found
+  int* children;  // [batch] new requests of each old one
+  int* kept;      // [batch] pages that the first of them keeps (the full ones among them)
+  int2* child;    // [new_batch] {fresh slots, pages before them}
+};
+
+struct PagesParams {
+  RowsGeom g;                 // batch, max_pages, num_slots, slot_stride, num_kv_heads, err, page_table, kv_lens
+  PagesWs ws;
+  uint8_t* pool;
+  const int32_t* ref;
+  const int32_t* num_pages;   // or null: those of kv_lens
+  const int32_t* parent;      // [new_batch], forking
+  const int32_t* new_tokens;  // [new_batch] or null
+  int32_t* new_ref;
+  int32_t* new_table;
+  int32_t* new_lens;
+  int32_t* new_num_pages;     // or null
+  int32_t* slot_map;          // compacting
+  int32_t* num_used;
+  int new_batch, chunks, buffers;
+  int row_bytes;              // of one head's row, 0: E2M1 blocks
+  int block_bytes;            // of one head's 32 rows
+};
+
+cudaError_t launch_pages_fork(const PagesParams& p, int sms, cudaStream_t st);
+cudaError_t launch_pages_compact(const PagesParams& p, int sms, cudaStream_t st);
+size_t pages_smem(int chunks, int new_batch);   // of the second kernel of each
+
+}  // namespace trtv

@@ -20,7 +20,7 @@ ROOT = os.path.dirname(HERE)
 
 SOURCES = ["abi.cu", "small_kernels.cu", "attn_bf16.cu", "attn_fp8.cu", "attn_pm.cu", "proxy_bf16.cu",
            "proxy_fp8.cu", "abi_rows.cu", "row_kernels.cu", "rows_attn_bf16.cu",
-           "rows_attn_fp8.cu", "rows_attn_fp4.cu", "abi_pages.cu", "pages.cu"]
+           "rows_attn_fp8.cu", "rows_attn_fp4.cu", "rows_few.cu", "abi_pages.cu", "pages.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr",
          "-I" + os.path.join(ROOT, "include")]

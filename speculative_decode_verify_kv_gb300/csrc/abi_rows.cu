@@ -27,6 +27,7 @@ constexpr float kMinScale = 5.421011e-20f;  // 2^-64
 // 700-1500 17.0 / 15.6 / 16.1.  E4M3, at 64 / 128 / 256 / 384: 64 trees 113.1 / 110.8 /
 // 105.8 / 100.7, one over 700 14.4 / 14.5 / 15.0 / 14.4, one over 16000 30.0 at each.
 constexpr int kRowsSetupTwo = 256, kRowsSetupTwoFp8 = 512, kRowsSetupOne = 128, kRowsSetupOneFp8 = 256;
+constexpr int kFewSetup = 256;
 
 // Geometry checks shared by the packed-row calls.
 trtv_status rows_geom(const trtv_geom* g, const int32_t* indptr, int32_t num_tokens, RowsGeom* r) {
@@ -77,6 +78,8 @@ trtv_status rows_device(RowsGeom* r, const int32_t* page_table, const int32_t* k
 // What one attention call needs besides its pointers.
 struct RowsPlan {
   bool two;            // 256-row items
+  int few;             // E2M1, at most 16 * few rows an item: rows_few.cuh; else 0
+  int rows;            // of an item's piece in the workspace
   int num_ctas;
   size_t ws_o, ws_lse, ws_splits, ws_cont, ws_total;
 };
@@ -87,9 +90,13 @@ struct RowsPlan {
 bool rows_plan(const trtv_geom* g, const RowsGeom& r, RowsPlan* pl) {
   const int tile_toks = kRowsTile / r.group;
   pl->two = g->qo_len > tile_toks;
+  pl->few = 0;
+  if (g->kv_dtype == TRTV_FP4_E2M1 && static_cast<int64_t>(r.group) * g->qo_len <= 32)
+    pl->few = r.group * g->qo_len <= 16 ? 1 : 2;
+  pl->rows = pl->few > 0 ? 16 * pl->few : pl->two ? 2 * kRowsTile : kRowsTile;
   pl->num_ctas = g->num_ctas > 0 ? g->num_ctas : sm_count();
   if (pl->num_ctas <= 0) return false;
-  const size_t rows = pl->two ? 2 * kRowsTile : kRowsTile, pieces = 2 * static_cast<size_t>(pl->num_ctas);
+  const size_t rows = pl->rows, pieces = 2 * static_cast<size_t>(pl->num_ctas);
   size_t off = 0;
   pl->ws_o = off;
   off = align_up(off + pieces * rows * g->head_dim * sizeof(float), 256);
@@ -106,7 +113,7 @@ bool rows_plan(const trtv_geom* g, const RowsGeom& r, RowsPlan* pl) {
 // Shared memory: Q (one or two tiles), the page ring, E4M3 and E2M1: the codes' ring, the
 // groups' exchange, the pieces, the requests' scan and its 32 warp totals,
 // barriers.  The ring takes what is left, at most kMaxStages pages.
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 8, kFewStages = 16;
 bool rows_smem(const trtv_geom* g, const RowsPlan& pl, RowsAttnParams* p, size_t* bytes) {
   const bool codes = g->kv_dtype != TRTV_BF16;
   const size_t tile = static_cast<size_t>(kRowsTile) * g->head_dim * 2;
@@ -137,6 +144,39 @@ bool rows_smem(const trtv_geom* g, const RowsPlan& pl, RowsAttnParams* p, size_t
   off += p->nst * tile;
   p->off_raw = static_cast<int>(off);
   off += raw_ring;
+  p->off_ml = static_cast<int>(off);
+  off += ml;
+  p->off_pieces = static_cast<int>(off);
+  off += pieces;
+  p->off_scan = static_cast<int>(off);
+  off += scan;
+  p->off_bar = static_cast<int>(off);
+  off += bars;
+  *bytes = off + kAlignSlack;
+  return true;
+}
+
+// Few rows: two pieces' Q, the ring of pages (K and V together), the consumers'
+// shares of O and their maxima and sums, the pieces, the scan, barriers.
+bool few_smem(const trtv_geom* g, const RowsPlan& pl, RowsAttnParams* p, size_t* bytes) {
+  const FewShape f = few_shape(g->head_dim, pl.few);
+  const size_t page = 2 * static_cast<size_t>(kGroups) * kFp4Row * g->head_dim;
+  const size_t scan = align_up((static_cast<size_t>(g->batch) + 1 + 32) * sizeof(int64_t), 16);
+  const size_t q = align_up(2 * static_cast<size_t>(f.q_bytes), 128);
+  const size_t rows = static_cast<size_t>(f.consumers) * 16 * pl.few, share = rows * g->head_dim * sizeof(float), ml = rows * 2 * sizeof(float);
+  const size_t pieces = 4 * 48, bars = (2 * kFewStages + 16) * sizeof(uint64_t);
+  const size_t fixed = q + share + ml + pieces + scan + bars + kAlignSlack;
+  // (whole sets: a stage's pages are then always the same warps', whose parities cannot fall two phases behind)
+  p->nst = static_cast<int>(std::min<size_t>(fixed < kSmemOptin ? (kSmemOptin - fixed) / page : 0, kFewStages)) / f.sets * f.sets;
+  if (p->nst == 0) return false;
+  p->nraw = 0;
+  size_t off = 0;
+  p->off_ring = 0;
+  off += p->nst * page;
+  p->off_q = static_cast<int>(off);
+  off += q;
+  p->off_raw = static_cast<int>(off);
+  off += share;
   p->off_ml = static_cast<int>(off);
   off += ml;
   p->off_pieces = static_cast<int>(off);
@@ -192,17 +232,19 @@ trtv_status rows_attn(const trtv_geom* g, const void* q, const void* pool, const
   if (!rows_plan(g, p.g, &pl)) return TRTV_ERR_CUDA;
   if (ws == nullptr || !aligned(ws, 256) || ws_bytes < pl.ws_total) return TRTV_ERR_WORKSPACE;
   size_t smem = 0;
-  if (!rows_smem(g, pl, &p, &smem)) return TRTV_ERR_UNSUPPORTED;
+  if (pl.few > 0 ? !few_smem(g, pl, &p, &smem) : !rows_smem(g, pl, &p, &smem)) return TRTV_ERR_UNSUPPORTED;
   if ((s = rows_device(&p.g, page_table, kv_lens)) != TRTV_OK) return s;
   p.tile_toks = kRowsTile / p.g.group;
   p.items = mask != nullptr && pl.two ? (g->qo_len + 2 * p.tile_toks - 1) / (2 * p.tile_toks) : 1;
   if (p.items > pl.num_ctas) p.items = 1;
-  CUtensorMap kv_map{}, q_map;
+  CUtensorMap kv_map{}, q_map{};
   const bool fp4 = g->kv_dtype == TRTV_FP4_E2M1;
-  if ((!fp4 && !encode_pages(g, pool, &kv_map)) || !encode_rows(g, p.g, p.tile_toks, q, &q_map)) return TRTV_ERR_CUDA;
+  if ((!fp4 && !encode_pages(g, pool, &kv_map)) || (pl.few == 0 && !encode_rows(g, p.g, p.tile_toks, q, &q_map)))
+    return TRTV_ERR_CUDA;
   uint8_t* wsb = static_cast<uint8_t*>(ws);
   p.tree_mask = mask;
   p.pool = static_cast<const uint8_t*>(pool);
+  p.q = static_cast<const __nv_bfloat16*>(q);
   p.mask_words = (g->qo_len + 31) / 32;
   p.out = out;
   p.ws_o = reinterpret_cast<float*>(wsb + pl.ws_o);
@@ -212,16 +254,17 @@ trtv_status rows_attn(const trtv_geom* g, const void* q, const void* pool, const
   p.out_f32 = out_dtype == TRTV_F32;
   p.num_ctas = pl.num_ctas;
   const bool codes = g->kv_dtype != TRTV_BF16;
-  p.setup = pl.two ? (codes ? kRowsSetupTwoFp8 : kRowsSetupTwo) : codes ? kRowsSetupOneFp8 : kRowsSetupOne;
+  p.setup = pl.few > 0 ? kFewSetup : pl.two ? (codes ? kRowsSetupTwoFp8 : kRowsSetupTwo) : codes ? kRowsSetupOneFp8 : kRowsSetupOne;
   p.scale_log2 = g->sm_scale * g->k_scale * 1.4426950408889634f;
   p.v_scale = g->v_scale;
   p.wait_ns = wait_limit_ns();
   p.withhold = withheld_pages();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = fp4     ? launch_rows_attn_fp4(g->head_dim, pl.two, kv_map, q_map, p, smem, st)
+  cudaError_t e = pl.few > 0 ? launch_rows_few(g->head_dim, pl.few, p, smem, st)
+                  : fp4   ? launch_rows_attn_fp4(g->head_dim, pl.two, kv_map, q_map, p, smem, st)
                   : codes ? launch_rows_attn_fp8(pl.two, kv_map, q_map, p, smem, st)
                           : launch_rows_attn_bf16(g->head_dim, pl.two, kv_map, q_map, p, smem, st);
-  if (e == cudaSuccess) e = launch_rows_join(g->head_dim, pl.two, p, st);
+  if (e == cudaSuccess) e = launch_rows_join(g->head_dim, pl.rows, p, st);
   return e == cudaSuccess ? TRTV_OK : TRTV_ERR_CUDA;
 }
 
@@ -313,7 +356,8 @@ size_t trtv_workspace_bytes_rows(const trtv_geom* geom) {
   RowsAttnParams p{};
   size_t smem = 0;
   const int32_t any = 0;  // (rows are not checked: a host pointer that nothing reads)
-  if (rows_geom(geom, &any, 0, &r) != TRTV_OK || !rows_plan(geom, r, &pl) || !rows_smem(geom, pl, &p, &smem)) return 0;
+  if (rows_geom(geom, &any, 0, &r) != TRTV_OK || !rows_plan(geom, r, &pl)) return 0;
+  if (pl.few > 0 ? !few_smem(geom, pl, &p, &smem) : !rows_smem(geom, pl, &p, &smem)) return 0;
   return pl.ws_total;
 }
 

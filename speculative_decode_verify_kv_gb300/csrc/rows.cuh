@@ -163,6 +163,7 @@ struct RowsAttnParams {
   RowsGeom g;
   const uint32_t* tree_mask;   // [num_tokens, mask_words] or null: the causal bound
   const uint8_t* pool;         // E2M1 caches (others: the tensor map)
+  const __nv_bfloat16* q;      // few rows (others: the tensor map)
   void* out;
   float* ws_o;                 // [2 * num_ctas, rows, D] pieces, each normalised by its own sum
   float* ws_lse;               // [2 * num_ctas, rows] log2 of their sums
@@ -187,7 +188,14 @@ cudaError_t launch_rows_attn_fp8(bool two, const CUtensorMap& kv_map, const CUte
                                  const RowsAttnParams& p, size_t smem, cudaStream_t st);
 cudaError_t launch_rows_attn_fp4(int head_dim, bool two, const CUtensorMap& kv_map, const CUtensorMap& q_map,
                                  const RowsAttnParams& p, size_t smem, cudaStream_t st);
-cudaError_t launch_rows_join(int head_dim, bool two, const RowsAttnParams& p, cudaStream_t st);
+// E2M1 caches, at most 16 mt rows per (request, KV head), mt 1 or 2
+cudaError_t launch_rows_few(int head_dim, int mt, const RowsAttnParams& p, size_t smem, cudaStream_t st);
+struct FewShape {
+  int consumers, q_bytes, sets;   // warps that its pieces are joined over; shared memory of a piece's Q; pages at a time
+};
+FewShape few_shape(int head_dim, int mt);
+// rows: of a piece in the workspace
+cudaError_t launch_rows_join(int head_dim, int rows, const RowsAttnParams& p, cudaStream_t st);
 cudaError_t launch_read_kv(int head_dim, int kv_dtype, const ReadParams& p, cudaStream_t st);
 cudaError_t launch_norm_rope_stage(int head_dim, int kv_dtype, const NormRopeParams& p, cudaStream_t st);
 cudaError_t launch_tree_commit(int head_dim, int kv_dtype, const CommitParams& p, cudaStream_t st);

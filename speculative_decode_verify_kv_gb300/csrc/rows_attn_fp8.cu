@@ -94,14 +94,20 @@ __global__ void __launch_bounds__(kJoinThreads, 4) rows_join_kernel(const __grid
   }
 }
 
-cudaError_t launch_rows_join(int head_dim, bool two, const RowsAttnParams& p, cudaStream_t st) {
+template <int D>
+cudaError_t launch_join_kind(int rows, const RowsAttnParams& p, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>(p.num_ctas) * (rows / kJoinRows)), block(kJoinThreads);
+  switch (rows) {
+    case 16: return launch_pdl(rows_join_kernel<D, 16>, grid, block, 0, st, p);
+    case 32: return launch_pdl(rows_join_kernel<D, 32>, grid, block, 0, st, p);
+    case 128: return launch_pdl(rows_join_kernel<D, 128>, grid, block, 0, st, p);
+    default: return launch_pdl(rows_join_kernel<D, 256>, grid, block, 0, st, p);
+  }
+}
+
+cudaError_t launch_rows_join(int head_dim, int rows, const RowsAttnParams& p, cudaStream_t st) {
   if (p.num_ctas < 2) return cudaSuccess;  // nothing is cut
-  const dim3 grid(static_cast<unsigned>(p.num_ctas) * (two ? 256 : 128) / kJoinRows), block(kJoinThreads);
-  if (head_dim == 64)
-    return two ? launch_pdl(rows_join_kernel<64, 256>, grid, block, 0, st, p)
-               : launch_pdl(rows_join_kernel<64, 128>, grid, block, 0, st, p);
-  return two ? launch_pdl(rows_join_kernel<128, 256>, grid, block, 0, st, p)
-             : launch_pdl(rows_join_kernel<128, 128>, grid, block, 0, st, p);
+  return head_dim == 64 ? launch_join_kind<64>(rows, p, st) : launch_join_kind<128>(rows, p, st);
 }
 
 }  // namespace trtv

@@ -204,6 +204,19 @@ bool encode_pages(const trtv_geom* g, const void* pool, CUtensorMap* map) {
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The E2M1 pool as [sub-pages][KV heads][a block's lines of 128 bytes]: a box is
+// one head's blocks of `subs` sub-pages (4: a page of K or V, 8: of both).
+bool encode_blocks(const trtv_geom* g, const void* pool, int subs, CUtensorMap* map) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encoder();
+  if (enc == nullptr) return false;
+  const cuuint64_t block = static_cast<cuuint64_t>(kFp4Row) * g->head_dim, Hk = g->num_kv_heads;
+  cuuint64_t dims[4] = {128, block / 128, Hk, static_cast<cuuint64_t>(g->num_slots) * g->slot_stride * kGroups};
+  cuuint64_t strides[3] = {128, block, Hk * block};
+  cuuint32_t box[4] = {128, static_cast<cuuint32_t>(block / 128), 1, static_cast<cuuint32_t>(subs)}, estr[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(pool), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+             CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // q as [rows][query heads][head_dim]: a box is one tile's 64-column block (its
 // tokens' heads of one group).
 bool encode_rows(const trtv_geom* g, const RowsGeom& r, int tile_toks, const void* q, CUtensorMap* map) {
@@ -237,13 +250,12 @@ trtv_status rows_attn(const trtv_geom* g, const void* q, const void* pool, const
   p.tile_toks = kRowsTile / p.g.group;
   p.items = mask != nullptr && pl.two ? (g->qo_len + 2 * p.tile_toks - 1) / (2 * p.tile_toks) : 1;
   if (p.items > pl.num_ctas) p.items = 1;
-  CUtensorMap kv_map{}, q_map{};
+  CUtensorMap kv_map, q_map{};
   const bool fp4 = g->kv_dtype == TRTV_FP4_E2M1;
-  if ((!fp4 && !encode_pages(g, pool, &kv_map)) || (pl.few == 0 && !encode_rows(g, p.g, p.tile_toks, q, &q_map)))
+  if (!(fp4 ? encode_blocks(g, pool, pl.few > 0 ? 2 * kGroups : kGroups, &kv_map) : encode_pages(g, pool, &kv_map)) || (pl.few == 0 && !encode_rows(g, p.g, p.tile_toks, q, &q_map)))
     return TRTV_ERR_CUDA;
   uint8_t* wsb = static_cast<uint8_t*>(ws);
   p.tree_mask = mask;
-  p.pool = static_cast<const uint8_t*>(pool);
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.mask_words = (g->qo_len + 31) / 32;
   p.out = out;
@@ -260,7 +272,7 @@ trtv_status rows_attn(const trtv_geom* g, const void* q, const void* pool, const
   p.wait_ns = wait_limit_ns();
   p.withhold = withheld_pages();
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = pl.few > 0 ? launch_rows_few(g->head_dim, pl.few, p, smem, st)
+  cudaError_t e = pl.few > 0 ? launch_rows_few(g->head_dim, pl.few, kv_map, p, smem, st)
                   : fp4   ? launch_rows_attn_fp4(g->head_dim, pl.two, kv_map, q_map, p, smem, st)
                   : codes ? launch_rows_attn_fp8(pl.two, kv_map, q_map, p, smem, st)
                           : launch_rows_attn_bf16(g->head_dim, pl.two, kv_map, q_map, p, smem, st);

@@ -162,7 +162,6 @@ struct __align__(16) RowsSplit {
 struct RowsAttnParams {
   RowsGeom g;
   const uint32_t* tree_mask;   // [num_tokens, mask_words] or null: the causal bound
-  const uint8_t* pool;         // E2M1 caches (others: the tensor map)
   const __nv_bfloat16* q;      // few rows (others: the tensor map)
   void* out;
   float* ws_o;                 // [2 * num_ctas, rows, D] pieces, each normalised by its own sum
@@ -189,7 +188,7 @@ cudaError_t launch_rows_attn_fp8(bool two, const CUtensorMap& kv_map, const CUte
 cudaError_t launch_rows_attn_fp4(int head_dim, bool two, const CUtensorMap& kv_map, const CUtensorMap& q_map,
                                  const RowsAttnParams& p, size_t smem, cudaStream_t st);
 // E2M1 caches, at most 16 mt rows per (request, KV head), mt 1 or 2
-cudaError_t launch_rows_few(int head_dim, int mt, const RowsAttnParams& p, size_t smem, cudaStream_t st);
+cudaError_t launch_rows_few(int head_dim, int mt, const CUtensorMap& kv_map, const RowsAttnParams& p, size_t smem, cudaStream_t st);
 struct FewShape {
   int consumers, q_bytes, sets;   // warps that its pieces are joined over; shared memory of a piece's Q; pages at a time
 };

@@ -268,19 +268,21 @@ __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32
       : "r"(w));
 }
 
-// Bytes [src, src + bytes) of global memory, both ends and dst 16-byte aligned.
+// E2M1: one head's blocks of the sub-pages from `sub` on, as many as the map's box has.
 template <bool ONCE>
-__device__ __forceinline__ void bulk_load(void* dst, const uint8_t* src, int bytes, uint64_t* bar, uint64_t evict_first) {
+__device__ __forceinline__ void tma_load_blocks(void* dst, const CUtensorMap* map, uint64_t* bar, int h, int sub, uint64_t evict_first) {
   if constexpr (ONCE) {
     asm volatile(
-        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
-            smem_u32(dst)),
-        "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(evict_first)
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %2, %3, %4}], [%5], %6;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(h), "r"(sub), "r"(smem_u32(bar)), "l"(evict_first)
         : "memory");
   } else {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4}], [%5];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(h), "r"(sub), "r"(smem_u32(bar))
+        : "memory");
   }
 }
 
@@ -600,7 +602,7 @@ __global__ void __launch_bounds__(KV != TRTV_BF16 ? 512 : 384, 1)
     }
   } else if (warp == 8) {
     // ------------------------------------------------------------ page loads
-    if (!FP4 && lane == 0) prefetch_tensormap(&kv_map);
+    if (lane == 0) prefetch_tensormap(&kv_map);
     const int64_t vbuf = kGroups;
     const uint64_t pol = policy_evict_first();
     RowsPiece it{};
@@ -644,13 +646,9 @@ __global__ void __launch_bounds__(KV != TRTV_BF16 ? 512 : 384, 1)
             if (lane == 0) {
               if (i >= NRAW) ok = rows_wait(&rawfree[st], static_cast<uint32_t>(i / NRAW - 1) & 1u, wt);
               if (ok) {
-                if constexpr (FP4) {   // the sub-pages that hold positions below kv_len
-                  const int used = min(kGroups, (it.ctx + it.n - j * kPage + kSub - 1) / kSub);
-                  const int64_t pitch = static_cast<int64_t>(g.num_kv_heads) * GROUPS4;
-                  const uint8_t* src = p.pool + (sub + kv * vbuf) * pitch + static_cast<int64_t>(it.h) * GROUPS4;
-                  mbar_arrive_expect_tx(&raw[st], used * GROUPS4);
-                  for (int gr = 0; gr < used; ++gr)
-                    bulk_load<!TWO>(rring + st * RAW + gr * GROUPS4, src + gr * pitch, GROUPS4, &raw[st], pol);
+                if constexpr (FP4) {
+                  mbar_arrive_expect_tx(&raw[st], RAW);
+                  tma_load_blocks<!TWO>(rring + st * RAW, &kv_map, &raw[st], it.h, static_cast<int>(sub + kv * vbuf), pol);
                 } else {
                   mbar_arrive_expect_tx(&raw[st], RAW);
                   tma_load_page<!TWO>(rring + st * RAW, &kv_map, &raw[st], 0, it.h, static_cast<int>(sub + kv * vbuf), pol);

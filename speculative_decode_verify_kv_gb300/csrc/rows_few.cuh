@@ -64,7 +64,7 @@ __device__ __forceinline__ void set_registers() {
 
 template <int D, int MT>
 __global__ void __launch_bounds__(few_threads(D, MT), 1)
-    rows_few_kernel(const __grid_constant__ RowsAttnParams p) {
+    rows_few_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ RowsAttnParams p) {
   constexpr int CW = few_warps(D, MT);
   constexpr int BLOCK = kFp4Row * D;           // bytes of 32 rows of a head
   constexpr int HALF = kGroups * BLOCK;        // a page's K (or V)
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(few_threads(D, MT), 1)
     if (warp == CW) {
       // page loads
       const uint64_t pol = policy_evict_first();
-      const int64_t pitch = static_cast<int64_t>(g.num_kv_heads) * BLOCK;   // from one group's block of a head to the next's
+      if (lane == 0) prefetch_tensormap(&kv_map);
       int at = 0;
       uint32_t ph = 0;
       RowsPiece it{};
@@ -181,14 +181,9 @@ __global__ void __launch_bounds__(few_threads(D, MT), 1)
           if (stop) break;
           ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], eph, wt));
           if (!ok) break;
-          // (lane k: K's and V's group k % 4, those that hold positions below kv_len)
-          const int used = min(kGroups, (it.ctx + it.n - j * kPage + kSub - 1) / kSub);
-          if (lane == 0) mbar_arrive_expect_tx(&full[st], 2 * used * BLOCK);
-          __syncwarp();
-          if (lane < 2 * kGroups && lane % kGroups < used) {
-            const int gr = lane % kGroups, kv = lane / kGroups;
-            bulk_load<true>(ring + st * 2 * HALF + kv * HALF + gr * BLOCK,
-                            p.pool + (sub + kv * kGroups + gr) * pitch + static_cast<int64_t>(it.h) * BLOCK, BLOCK, &full[st], pol);
+          if (lane == 0) {   // (V's buffer follows K's: one box has both)
+            mbar_arrive_expect_tx(&full[st], 2 * HALF);
+            tma_load_blocks<true>(ring + st * 2 * HALF, &kv_map, &full[st], it.h, static_cast<int>(sub), pol);
           }
           ++i;
           if (++st == NST) {

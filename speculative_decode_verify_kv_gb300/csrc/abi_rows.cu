@@ -78,7 +78,7 @@ trtv_status rows_device(RowsGeom* r, const int32_t* page_table, const int32_t* k
 // What one attention call needs besides its pointers.
 struct RowsPlan {
   bool two;            // 256-row items
-  int few;             // E2M1, at most 16 * few rows an item: rows_few.cuh; else 0
+  int few;             // E2M1, at most 8 * few rows an item: rows_few.cuh; else 0
   int rows;            // of an item's piece in the workspace
   int num_ctas;
   size_t ws_o, ws_lse, ws_splits, ws_cont, ws_total;
@@ -92,8 +92,8 @@ bool rows_plan(const trtv_geom* g, const RowsGeom& r, RowsPlan* pl) {
   pl->two = g->qo_len > tile_toks;
   pl->few = 0;
   if (g->kv_dtype == TRTV_FP4_E2M1 && static_cast<int64_t>(r.group) * g->qo_len <= 32)
-    pl->few = r.group * g->qo_len <= 16 ? 1 : 2;
-  pl->rows = pl->few > 0 ? 16 * pl->few : pl->two ? 2 * kRowsTile : kRowsTile;
+    pl->few = r.group * g->qo_len <= 8 ? 1 : r.group * g->qo_len <= 16 ? 2 : 4;
+  pl->rows = pl->few > 0 ? 8 * pl->few : pl->two ? 2 * kRowsTile : kRowsTile;
   pl->num_ctas = g->num_ctas > 0 ? g->num_ctas : sm_count();
   if (pl->num_ctas <= 0) return false;
   const size_t rows = pl->rows, pieces = 2 * static_cast<size_t>(pl->num_ctas);
@@ -163,7 +163,7 @@ bool few_smem(const trtv_geom* g, const RowsPlan& pl, RowsAttnParams* p, size_t*
   const size_t page = 2 * static_cast<size_t>(kGroups) * kFp4Row * g->head_dim;
   const size_t scan = align_up((static_cast<size_t>(g->batch) + 1 + 32) * sizeof(int64_t), 16);
   const size_t q = align_up(2 * static_cast<size_t>(f.q_bytes), 128);
-  const size_t rows = static_cast<size_t>(f.consumers) * 16 * pl.few, share = rows * g->head_dim * sizeof(float), ml = rows * 2 * sizeof(float);
+  const size_t rows = static_cast<size_t>(f.consumers) * 8 * pl.few, share = rows * g->head_dim * sizeof(float), ml = rows * 2 * sizeof(float);
   const size_t pieces = 4 * 48, bars = (2 * kFewStages + 16) * sizeof(uint64_t);
   const size_t fixed = q + share + ml + pieces + scan + bars + kAlignSlack;
   // (whole sets: a stage's pages are then always the same warps', whose parities cannot fall two phases behind)

@@ -187,12 +187,12 @@ cudaError_t launch_rows_attn_fp8(bool two, const CUtensorMap& kv_map, const CUte
                                  const RowsAttnParams& p, size_t smem, cudaStream_t st);
 cudaError_t launch_rows_attn_fp4(int head_dim, bool two, const CUtensorMap& kv_map, const CUtensorMap& q_map,
                                  const RowsAttnParams& p, size_t smem, cudaStream_t st);
-// E2M1 caches, at most 16 mt rows per (request, KV head), mt 1 or 2
-cudaError_t launch_rows_few(int head_dim, int mt, const CUtensorMap& kv_map, const RowsAttnParams& p, size_t smem, cudaStream_t st);
+// E2M1 caches, at most 8 nr rows per (request, KV head), nr 1, 2 or 4
+cudaError_t launch_rows_few(int head_dim, int nr, const CUtensorMap& kv_map, const RowsAttnParams& p, size_t smem, cudaStream_t st);
 struct FewShape {
   int consumers, q_bytes, sets;   // warps that its pieces are joined over; shared memory of a piece's Q; pages at a time
 };
-FewShape few_shape(int head_dim, int mt);
+FewShape few_shape(int head_dim, int nr);
 // rows: of a piece in the workspace
 cudaError_t launch_rows_join(int head_dim, int rows, const RowsAttnParams& p, cudaStream_t st);
 cudaError_t launch_read_kv(int head_dim, int kv_dtype, const ReadParams& p, cudaStream_t st);

@@ -20,13 +20,14 @@ cudaError_t launch_rows_attn_fp8(bool two, const CUtensorMap& kv_map, const CUte
 // loaded (items of two pieces, 4 chunks of 300-512 tokens: 120.5 -> 117 us).  Batches
 // of two, six CTAs an SM: 115 us, but a tree cut into many pieces 16.5 -> 18.3.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 16;
+constexpr int kJoinRows = 16;   // (or all of a piece with fewer)
 
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads, 4) rows_join_kernel(const __grid_constant__ RowsAttnParams p) {
-  constexpr int F4 = D / 4, EL = kJoinRows * F4 / kJoinThreads, kBatch = 4;
+  constexpr int JR = ROWS < kJoinRows ? ROWS : kJoinRows;
+  constexpr int F4 = D / 4, EL = (JR * F4 + kJoinThreads - 1) / kJoinThreads, kBatch = 4;
   const RowsGeom& g = p.g;
-  const int c0 = blockIdx.x / (ROWS / kJoinRows), chunk = blockIdx.x % (ROWS / kJoinRows), tid = threadIdx.x;
+  const int c0 = blockIdx.x / (ROWS / JR), chunk = blockIdx.x % (ROWS / JR), tid = threadIdx.x;
   pdl_wait();
   pdl_trigger();
   // b, h, tok0, n | row0, c_last, stride
@@ -39,10 +40,10 @@ __global__ void __launch_bounds__(kJoinThreads, 4) rows_join_kernel(const __grid
   bool live[EL];
 #pragma unroll
   for (int u = 0; u < EL; ++u) {
-    row[u] = chunk * kJoinRows + (u * kJoinThreads + tid) / F4;
+    row[u] = min(chunk * JR + (u * kJoinThreads + tid) / F4, ROWS - 1);
     const int t = row[u] % kRowsTile / g.group;
     tok[u] = d0.z + (row[u] / kRowsTile) * p.tile_toks + t;
-    live[u] = t < p.tile_toks && tok[u] < d0.w;
+    live[u] = t < p.tile_toks && tok[u] < d0.w && (u * kJoinThreads + tid) / F4 < JR;
     m[u] = -INFINITY;
     l[u] = 0.f;
     acc[u] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -96,8 +97,9 @@ __global__ void __launch_bounds__(kJoinThreads, 4) rows_join_kernel(const __grid
 
 template <int D>
 cudaError_t launch_join_kind(int rows, const RowsAttnParams& p, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(p.num_ctas) * (rows / kJoinRows)), block(kJoinThreads);
+  const dim3 grid(static_cast<unsigned>(p.num_ctas) * (rows < kJoinRows ? 1 : rows / kJoinRows)), block(kJoinThreads);
   switch (rows) {
+    case 8: return launch_pdl(rows_join_kernel<D, 8>, grid, block, 0, st, p);
     case 16: return launch_pdl(rows_join_kernel<D, 16>, grid, block, 0, st, p);
     case 32: return launch_pdl(rows_join_kernel<D, 32>, grid, block, 0, st, p);
     case 128: return launch_pdl(rows_join_kernel<D, 128>, grid, block, 0, st, p);

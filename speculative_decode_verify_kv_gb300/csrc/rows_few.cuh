@@ -1,5 +1,5 @@
 // rows_few.cuh -- attention of few rows over E2M1 caches: decoding, verify steps
-// and small trees, at most 16 MT rows (tokens x query heads of one KV head).
+// and small trees, at most 8 NR rows (tokens x query heads of one KV head).
 //
 // A page's K and V are 18 KB of codes and scales against 64 KB in 16 bits, so
 // what matters is that nothing else passes through shared memory: a warp turns
@@ -7,17 +7,19 @@
 // (mma.sync m16n8k16, f16 operands, fp32 sums) and keeps scores, weights and
 // the output in registers.  Written out to shared memory for tcgen05, a page's
 // tiles cost 512 cycles of stores and as many of reads, above the 800 that its
-// bytes take to arrive at the SM's share of the copy rate; an E2M1 conversion,
+// bytes take to arrive at the SM's share of the copy rate.  An E2M1 conversion,
 // a permute and a product of f16 pairs take 2 cycles each per warp, 5 of them
-// per 4 elements.
+// per 4 elements, and an m16n8k16 8 (and 2 of the others').
 //
-// Fragments.  The order of the head dims inside QK^T, of the positions inside a
-// slice and of the columns of O is free as long as both operands agree, so each
-// lane reads what lies together: of a key a quarter of its dims (lane % 4), of a
-// value an eighth (lane / 4), whole scale blocks in both.  S = Q K^T leaves the
-// weights where P V wants its A operand.  Of 16 positions, column n of half i is
-// row 8 i + n / 2 + 4 (n % 2): lanes of one load then read neighbouring rows.
-// The code's scale is a factor of its f16 value, exact (see rows_attn.cuh).
+// Fragments.  Positions are the products' M, rows their N: S^T = K Q^T and
+// O^T += V^T P^T, so eight rows fill an instruction.  The order of the head dims
+// inside K Q^T, of the positions inside a tile and of the rows of O^T is free as
+// long as both operands agree, so each lane reads what lies together: of a key a
+// quarter of its dims (lane % 4), of a value an eighth (lane / 4), whole scale
+// blocks in both.  The weights become P V's B operand by one transposition of 8 x 8
+// f16 pairs (movmatrix) per 8 positions.  Position m of a tile's half is its row
+// m / 2 + 4 (m % 2): lanes of one load then read neighbouring rows.  The code's scale
+// is a factor of its f16 value, exact (see rows_attn.cuh).
 //
 // Each consumer warp has a running maximum, sum and O of its own over the slices
 // that it takes of each page (every SETS-th page of the CTA is its).  At the end of
@@ -26,7 +28,7 @@
 // pages.  Another warp prepares the next piece's Q: f16 in the order of the
 // fragments.  So a piece costs the consumers little more than its pages (joined
 // by all warps at a barrier, with Q loaded by each: 5.4 us a piece against 0.6 a
-// page, 64 requests' decoding 68 us).
+// page).
 // Work split, pieces, the join between CTAs and the refusals are rows_attn.cuh's,
 // with one item per (request, KV head).
 #pragma once
@@ -38,14 +40,21 @@ namespace trtv {
 constexpr int kFewLeast = 256;       // positions that a CTA takes at least
 
 constexpr int kFewMergers = 2;       // merging warps
+constexpr int align16(int x) { return (x + 15) / 16 * 16; }
 
-// Consumer warps, in whole warpgroups, tiles of 8 positions that one takes at a
-// time, and whether Q's fragments stay in its registers.
-constexpr int few_warps(int D, int MT) { return MT == 1 || D == 64 ? 12 : 8; }
-constexpr int few_tiles(int D, int MT) { return 4; }
-constexpr bool few_q_regs(int D, int MT) { return MT == 1; }
-constexpr int few_threads(int D, int MT) { return 32 * few_warps(D, MT) + 128; }
-constexpr int few_q_bytes(int D, int MT) { return MT * (D / 16) * 512 + MT * 64; }   // fragments and scales of a piece
+// Consumer warps, in whole warpgroups, the registers of a thread of theirs and of
+// the other four warps, tiles of 16 positions that a warp takes at a time, and
+// whether Q's fragments stay in its registers.
+constexpr int few_warps(int NR) { return NR == 1 ? 16 : NR == 2 ? 12 : 8; }
+constexpr int few_regs(int NR) { return NR == 1 ? 104 : NR == 2 ? 152 : 224; }
+constexpr int kFewOtherRegs = 56;
+constexpr int few_tiles(int NR) { return NR == 4 ? 1 : 2; }
+constexpr bool few_q_regs(int NR) { return NR == 1; }
+constexpr int few_threads(int NR) { return 32 * few_warps(NR) + 128; }
+constexpr int few_q_bytes(int D, int NR) { return NR * (D / 32) * 512 + align16(NR * 32); }   // fragments and scales of a piece
+constexpr bool few_registers_fit(int NR) {   // setmaxnreg draws on what the block was launched with
+  return 32 * few_warps(NR) * few_regs(NR) + 128 * kFewOtherRegs <= few_threads(NR) * (65536 / few_threads(NR) / 8 * 8);
+}
 
 // (not volatile: the compiler may move it among what it does not depend on)
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -56,26 +65,35 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) { return pack2<true>(lo, hi); }
 
+// 8 x 8 transposition of 16-bit elements over the warp
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
 template <int REGS, bool INC>
 __device__ __forceinline__ void set_registers() {
   if constexpr (INC) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
-template <int D, int MT>
-__global__ void __launch_bounds__(few_threads(D, MT), 1)
+template <int D, int NR>
+__global__ void __launch_bounds__(few_threads(NR), 1)
     rows_few_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ RowsAttnParams p) {
-  constexpr int CW = few_warps(D, MT);
+  constexpr int CW = few_warps(NR), ROWS = 8 * NR;
   constexpr int BLOCK = kFp4Row * D;           // bytes of 32 rows of a head
   constexpr int HALF = kGroups * BLOCK;        // a page's K (or V)
   constexpr int KW = D / 32;                   // words of codes that a lane takes of a key
   constexpr int VW = D / 64;                   // and of a value
-  constexpr int NT = D / 8;                    // n-tiles of O
-  constexpr int HT = few_tiles(D, MT);         // tiles of 8 positions that a warp takes at a time
-  constexpr int UPP = kPage / (8 * HT);        // of which a page has
+  constexpr int NT = D / 16;                   // tiles of 16 head dims of O
+  constexpr int HT = few_tiles(NR);            // tiles of 16 positions that a warp takes at a time
+  constexpr int UPP = kPage / (16 * HT);       // of which a page has
   constexpr int SETS = CW / UPP;               // pages at a time
-  constexpr bool QREG = few_q_regs(D, MT);
-  static_assert(CW % UPP == 0 && HT % 2 == 0, "whole pages");
+  constexpr bool QREG = few_q_regs(NR);
+  constexpr int QB = few_q_bytes(D, NR), QSCALE = NR * (D / 32) * 512;
+  static_assert(CW % UPP == 0, "whole pages");
+  static_assert(few_registers_fit(NR), "registers");
   const RowsGeom& g = p.g;
 
   extern __shared__ uint8_t smem_raw[];
@@ -95,12 +113,12 @@ __global__ void __launch_bounds__(few_threads(D, MT), 1)
   RowsPiece* pieces = reinterpret_cast<RowsPiece*>(smem + p.off_pieces);
   uint8_t* ring = smem + p.off_ring;
   uint8_t* qbuf = smem + p.off_q;                                   // [2] fragments, then scales
-  float2* xml = reinterpret_cast<float2*>(smem + p.off_ml);         // [CW][16 MT] {reference maximum, sum}
-  float4* share = reinterpret_cast<float4*>(smem + p.off_raw);      // [CW][16 MT][D / 4] O of each consumer
+  float2* xml = reinterpret_cast<float2*>(smem + p.off_ml);         // [CW][ROWS] {reference maximum, sum}
+  float4* share = reinterpret_cast<float4*>(smem + p.off_raw);      // [CW][ROWS][D / 4] O of each consumer
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool causal = p.tree_mask == nullptr;
   // (chunk c of row r of O lies at c ^ swz: a warp's stores and loads fall into different banks)
-  auto swz = [](int r, int c) { return c ^ ((c >> (D == 128 ? 3 : 2)) | (r & 1) << 2); };
+  auto swz = [](int r, int c) { return c ^ ((r >> 1) & 3); };
 
   if (tid == 0) {
     for (int i = 0; i < NST; ++i) {
@@ -137,7 +155,7 @@ __global__ void __launch_bounds__(few_threads(D, MT), 1)
     }
   } else if (warp >= CW) {
     // ------------------------------------------------------------ producers
-    set_registers<56, false>();
+    set_registers<kFewOtherRegs, false>();
     if (warp == CW) {
       // page loads
       const uint64_t pol = policy_evict_first();
@@ -249,42 +267,47 @@ __global__ void __launch_bounds__(few_threads(D, MT), 1)
         if (seq >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&qempty[sl], static_cast<uint32_t>(seq / 2 - 1) & 1u, wt));
         if (!ok) break;
         const int gi = lane >> 2, t = lane & 3;
-        uint4* frag = reinterpret_cast<uint4*>(qbuf + sl * few_q_bytes(D, MT));
-        float* qscale = reinterpret_cast<float*>(qbuf + sl * few_q_bytes(D, MT) + MT * (D / 16) * 512);
+        uint4* frag = reinterpret_cast<uint4*>(qbuf + sl * QB);
+        float* qscale = reinterpret_cast<float*>(qbuf + sl * QB + QSCALE);
+        uint4 w[NR <= 2 ? NR : 2][D / 32];
+        constexpr int AT = NR <= 2 ? NR : 2;   // tiles of rows at a time
 #pragma unroll 1
-        for (int a = 0; a < MT; ++a) {
-          uint32_t v[2][D / 8];   // rows gi and gi + 8 of the tile, this lane's quarter
+        for (int a0 = 0; a0 < NR; a0 += AT) {
 #pragma unroll
-          for (int k2 = 0; k2 < 2; ++k2) {
-            const int r = gi + 8 * k2 + 16 * a, tk = r / g.group;
+          for (int a = 0; a < AT; ++a) {
+            const int r = 8 * (a0 + a) + gi, tk = r / g.group;
             const uint4* src = reinterpret_cast<const uint4*>(
                 p.q + ((static_cast<int64_t>(row0) + tk) * g.num_q_heads + h * g.group + (r - tk * g.group)) * D + t * (D / 4));
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-              const uint4 w = tk < n ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-              v[k2][4 * i] = w.x; v[k2][4 * i + 1] = w.y; v[k2][4 * i + 2] = w.z; v[k2][4 * i + 3] = w.w;
-            }
+            for (int i = 0; i < D / 32; ++i) w[a][i] = tk < n ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
           }
 #pragma unroll
-          for (int k2 = 0; k2 < 2; ++k2) {
+          for (int a = 0; a < AT; ++a) {
             // a power of two that brings the row's largest magnitude to [2^14, 2^15)
             // (rows below 2^-40 are taken as 2^-40: the scale stays a normal number)
             float amax = 0.f;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-              amax = max3(amax, fabsf(__uint_as_float(v[k2][i] << 16)), fabsf(__uint_as_float(v[k2][i] & 0xFFFF0000u)));
+            for (int i = 0; i < D / 32; ++i) {
+              const uint32_t v[4] = {w[a][i].x, w[a][i].y, w[a][i].z, w[a][i].w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                amax = max3(amax, fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xFFFF0000u)));
+            }
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
             const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -40);
             const float mul = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-            if (t == 0) qscale[gi + 8 * k2 + 16 * a] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
+            if (t == 0) qscale[8 * (a0 + a) + gi] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
+            // steps 2 i and 2 i + 1 of this lane's row: the products' B operand
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i)
-              v[k2][i] = pack_f16(__uint_as_float(v[k2][i] << 16) * mul, __uint_as_float(v[k2][i] & 0xFFFF0000u) * mul);
+            for (int i = 0; i < D / 32; ++i) {
+              uint32_t v[4] = {w[a][i].x, w[a][i].y, w[a][i].z, w[a][i].w};
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                v[x] = pack_f16(__uint_as_float(v[x] << 16) * mul, __uint_as_float(v[x] & 0xFFFF0000u) * mul);
+              frag[((a0 + a) * (D / 32) + i) * 32 + lane] = make_uint4(v[0], v[1], v[2], v[3]);
+            }
           }
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            frag[(a * (D / 16) + ks) * 32 + lane] = make_uint4(v[0][2 * ks], v[1][2 * ks], v[0][2 * ks + 1], v[1][2 * ks + 1]);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&qfull[sl]);
@@ -315,7 +338,7 @@ __global__ void __launch_bounds__(few_threads(D, MT), 1)
           float top = -INFINITY, lt = 0.f;
           float2 x[CW];
 #pragma unroll
-          for (int w = 0; w < CW; ++w) x[w] = xml[w * 16 * MT + r];
+          for (int w = 0; w < CW; ++w) x[w] = xml[w * ROWS + r];
 #pragma unroll
           for (int w = 0; w < CW; ++w) top = fmaxf(top, x[w].y == 0.f ? -INFINITY : x[w].x);
 #pragma unroll
@@ -325,12 +348,12 @@ __global__ void __launch_bounds__(few_threads(D, MT), 1)
           }
           const float f = lt == 0.f ? 0.f : (whole ? p.v_scale : 1.f) / lt;   // a NaN stays one
 #pragma unroll
-          for (int w = 0; w < CW; ++w) xml[w * 16 * MT + r].x = x[w].x * f;
-          if (!whole) p.ws_lse[slot * 16 * MT + r] = lt == 0.f ? -INFINITY : top + __log2f(lt);
+          for (int w = 0; w < CW; ++w) xml[w * ROWS + r].x = x[w].x * f;
+          if (!whole) p.ws_lse[slot * ROWS + r] = lt == 0.f ? -INFINITY : top + __log2f(lt);
         }
         __syncwarp();
         for (int r0 = mw * RPW; r0 < rows; r0 += kFewMergers * RPW) {
-          const int r = min(r0 + rr, 16 * MT - 1), tk = r / g.group;   // (beyond the rows: read, not written)
+          const int r = min(r0 + rr, ROWS - 1), tk = r / g.group;   // (beyond the rows: read, not written)
           float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int w0 = 0; w0 < CW; w0 += 4) {
@@ -338,8 +361,8 @@ __global__ void __launch_bounds__(few_threads(D, MT), 1)
             float4 v[4];
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              f[w] = xml[(w0 + w) * 16 * MT + r].x;
-              v[w] = share[((w0 + w) * 16 * MT + r) * C4 + swz(r, c)];
+              f[w] = xml[(w0 + w) * ROWS + r].x;
+              v[w] = share[((w0 + w) * ROWS + r) * C4 + swz(r, c)];
             }
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
@@ -349,7 +372,7 @@ __global__ void __launch_bounds__(few_threads(D, MT), 1)
           }
           if (r0 + rr >= rows) continue;
           if (!whole) {
-            *reinterpret_cast<float4*>(p.ws_o + (slot * 16 * MT + r) * D + 4 * c) = a;
+            *reinterpret_cast<float4*>(p.ws_o + (slot * ROWS + r) * D + 4 * c) = a;
           } else {
             const int64_t at = (static_cast<int64_t>(row0 + tk) * g.num_q_heads + h * g.group + (r - tk * g.group)) * D + 4 * c;
             if (p.out_f32) *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = a;
@@ -363,7 +386,7 @@ __global__ void __launch_bounds__(few_threads(D, MT), 1)
     }
   } else {
     // ------------------------------------------------------------ consumers
-    set_registers<CW == 12 ? 152 : 224, true>();
+    set_registers<few_regs(NR), true>();
     const int gi = lane >> 2, t = lane & 3;       // fragment row (or column), and place in it
     constexpr float LIFT = kRowsLiftF16;
     const int kpos = (gi >> 1) + 4 * (gi & 1);    // this lane's key of a half slice
@@ -380,32 +403,33 @@ __global__ void __launch_bounds__(few_threads(D, MT), 1)
       if (lane == 0) mbar_arrive(&iempty[pk]);
       if (j1 == 0) break;
       const int qs = seq & 1;
-      const uint4* frag = reinterpret_cast<const uint4*>(qbuf + qs * few_q_bytes(D, MT)) + lane;
-      const float* qscale = reinterpret_cast<const float*>(qbuf + qs * few_q_bytes(D, MT) + MT * (D / 16) * 512);
+      const uint4* frag = reinterpret_cast<const uint4*>(qbuf + qs * QB) + lane;
+      const float* qscale = reinterpret_cast<const float*>(qbuf + qs * QB + QSCALE);
       if (!__all_sync(0xffffffffu, mbar_wait(&qfull[qs], static_cast<uint32_t>(seq / 2) & 1u, wt))) break;
-      uint4 q[QREG ? MT : 1][QREG ? D / 16 : 1];
+      uint4 q[QREG ? NR : 1][QREG ? D / 32 : 1];
       if constexpr (QREG) {
 #pragma unroll
-        for (int a = 0; a < MT; ++a)
+        for (int a = 0; a < NR; ++a)
 #pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks) q[a][ks] = frag[(a * (D / 16) + ks) * 32];
+          for (int i = 0; i < D / 32; ++i) q[a][i] = frag[(a * (D / 32) + i) * 32];
       }
-      // rows of this lane: gi + 8 k, k < 2 MT
-      float scale[2 * MT], negm[2 * MT], lim[2 * MT], l[2 * MT];   // negm: LIFT - maximum scale; lim: when the maximum moves
+      // rows of this lane: 8 a + 2 t + c, at k = 2 a + c; negm: LIFT - maximum scale
+      float scale[2 * NR], negm[2 * NR], l[2 * NR];
 #pragma unroll
-      for (int k = 0; k < 2 * MT; ++k) {
-        scale[k] = qscale[gi + 8 * k];
-        lim[k] = -INFINITY;
+      for (int k = 0; k < 2 * NR; ++k) {
+        scale[k] = qscale[8 * (k >> 1) + 2 * t + (k & 1)];
         negm[k] = LIFT;
         l[k] = 0.f;
       }
+      bool unset = true;   // some row has no maximum yet (its negm is LIFT)
+      uint32_t has = 0;    // rows that have one
       if constexpr (QREG) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&qempty[qs]);
       }
-      float o[MT][NT][4];
+      float o[NR][NT][4];   // [.][b][2 e + c]: dim (D / 8) gi + 2 b + e, row 2 t + c
 #pragma unroll
-      for (int a = 0; a < MT; ++a)
+      for (int a = 0; a < NR; ++a)
 #pragma unroll
         for (int b = 0; b < NT; ++b)
 #pragma unroll
@@ -421,124 +445,139 @@ __global__ void __launch_bounds__(few_threads(D, MT), 1)
       }
 #pragma unroll 1
       for (; j < j1; j += SETS) {
-        const int pos0 = j * kPage + slice * (8 * HT);
+        const int pos0 = j * kPage + slice * (16 * HT);
         dead = __any_sync(0xffffffffu, !mbar_wait(&full[st], ph, wt));
         if (dead) break;
         if (pos0 < len) {
-          const uint8_t* kb = ring + st * 2 * HALF + slice * (8 * HT) / kSub * BLOCK;
+          const uint8_t* kb = ring + st * 2 * HALF + slice * (16 * HT) / kSub * BLOCK;
           const uint8_t* vb = kb + HALF;
-          constexpr int IN = kSub / (8 * HT);       // units of a 32-row block
-          const int r0 = IN == 1 ? 0 : slice % IN * (8 * HT);
-          const bool masked = pos0 + 8 * HT > open;
-          // ---- S = Q K^T
-          float s[MT][HT][4];
-          uint32_t kw[HT][KW], ks[HT][2];
+          constexpr int IN = kSub / (16 * HT);      // units of a 32-row block
+          const int r0 = IN == 1 ? 0 : slice % IN * (16 * HT);
+          const bool masked = pos0 + 16 * HT > open;
+          // ---- S^T = K Q^T
+          float s[HT][NR][4];   // [i][a][2 e + c]: position 8 e + gi of tile i, row 8 a + 2 t + c
+          uint32_t kw[HT][2][KW], ks[HT][2][2];
 #pragma unroll
           for (int i = 0; i < HT; ++i) {
-            const int r = r0 + 8 * i + kpos;
-            if constexpr (KW == 4) {
-              const uint4 v = *reinterpret_cast<const uint4*>(kb + r * (D / 2) + t * 16);
-              kw[i][0] = v.x; kw[i][1] = v.y; kw[i][2] = v.z; kw[i][3] = v.w;
-            } else {
-              const uint2 v = *reinterpret_cast<const uint2*>(kb + r * (D / 2) + t * 8);
-              kw[i][0] = v.x; kw[i][1] = v.y;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const int r = r0 + 16 * i + 8 * e + kpos;
+              if constexpr (KW == 4) {
+                const uint4 v = *reinterpret_cast<const uint4*>(kb + r * (D / 2) + t * 16);
+                kw[i][e][0] = v.x; kw[i][e][1] = v.y; kw[i][e][2] = v.z; kw[i][e][3] = v.w;
+              } else {
+                const uint2 v = *reinterpret_cast<const uint2*>(kb + r * (D / 2) + t * 8);
+                kw[i][e][0] = v.x; kw[i][e][1] = v.y;
+              }
+              const uint32_t two = e4m3x2_to_f16x2_reg(
+                  D == 128 ? *reinterpret_cast<const uint16_t*>(kb + kSub * (D / 2) + r * (D / 16) + t * 2)
+                           : kb[kSub * (D / 2) + r * (D / 16) + t]);
+              ks[i][e][0] = __byte_perm(two, 0, 0x1010);
+              ks[i][e][1] = __byte_perm(two, 0, 0x3232);
             }
-            const uint32_t two = e4m3x2_to_f16x2_reg(
-                D == 128 ? *reinterpret_cast<const uint16_t*>(kb + kSub * (D / 2) + r * (D / 16) + t * 2)
-                         : kb[kSub * (D / 2) + r * (D / 16) + t]);
-            ks[i][0] = __byte_perm(two, 0, 0x1010);
-            ks[i][1] = __byte_perm(two, 0, 0x3232);
 #pragma unroll
-            for (int a = 0; a < MT; ++a)
+            for (int a = 0; a < NR; ++a)
 #pragma unroll
-              for (int c = 0; c < 4; ++c) s[a][i][c] = 0.f;
+              for (int c = 0; c < 4; ++c) s[i][a][c] = 0.f;
           }
 #pragma unroll
           for (int x = 0; x < KW; ++x) {
-            uint32_t b[HT][4];
+            uint32_t b[HT][2][4];
 #pragma unroll
-            for (int i = 0; i < HT; ++i) {
-              e2m1x8_to_f16x8(kw[i][x], b[i]);
+            for (int i = 0; i < HT; ++i)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) b[i][e] = mul_f16x2(b[i][e], ks[i][D == 128 ? x >> 1 : 0]);
+              for (int e = 0; e < 2; ++e) {
+                e2m1x8_to_f16x8(kw[i][e][x], b[i][e]);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) b[i][e][y] = mul_f16x2(b[i][e][y], ks[i][e][D == 128 ? x >> 1 : 0]);
+              }
+            uint4 f[NR];
+#pragma unroll
+            for (int a = 0; a < NR; ++a) {
+              if constexpr (QREG) f[a] = q[a][x];
+              else f[a] = frag[(a * (D / 32) + x) * 32];
             }
             // (sums of different tiles in turn: each waits for its last product)
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+            for (int y = 0; y < 2; ++y)
 #pragma unroll
-              for (int a = 0; a < MT; ++a) {
-                uint4 f;
-                if constexpr (QREG) f = q[a][2 * x + e];
-                else f = frag[(a * (D / 16) + 2 * x + e) * 32];
-                const uint32_t fa[4] = {f.x, f.y, f.z, f.w};
+              for (int i = 0; i < HT; ++i) {
+                const uint32_t fa[4] = {b[i][0][2 * y], b[i][1][2 * y], b[i][0][2 * y + 1], b[i][1][2 * y + 1]};
 #pragma unroll
-                for (int i = 0; i < HT; ++i) mma_f16(s[a][i], fa, b[i][2 * e], b[i][2 * e + 1]);
+                for (int a = 0; a < NR; ++a) mma_f16(s[i][a], fa, y == 0 ? f[a].x : f[a].z, y == 0 ? f[a].y : f[a].w);
               }
           }
           if (masked) {
 #pragma unroll
-            for (int k = 0; k < 2 * MT; ++k) {
-              const int tok = (gi + 8 * k) / g.group;
+            for (int k = 0; k < 2 * NR; ++k) {
+              const int tok = (8 * (k >> 1) + 2 * t + (k & 1)) / g.group;
               const uint32_t* mask = causal ? nullptr : p.tree_mask + (static_cast<int64_t>(row0) + tok) * p.mask_words;
 #pragma unroll
               for (int i = 0; i < HT; ++i)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {   // column 2 t + c of tile i
-                  const int rel = pos0 + 8 * i + t + 4 * c - ctx;
+                for (int e = 0; e < 2; ++e) {
+                  const int rel = pos0 + 16 * i + 8 * e + kpos - ctx;
                   bool see = tok < n;
                   if (see && rel >= 0) see = causal ? rel <= tok : rel < n && (mask[rel >> 5] >> (rel & 31) & 1u);
-                  if (!see) s[k >> 1][i][2 * (k & 1) + c] = -INFINITY;
+                  if (!see) s[i][k >> 1][2 * e + (k & 1)] = -INFINITY;
                 }
             }
           }
           // ---- weights
-          bool grow = false;
-          float top[2 * MT];
+          bool grow = unset;
+          float top[2 * NR];
 #pragma unroll
-          for (int k = 0; k < 2 * MT; ++k) {
-            const int c = 2 * (k & 1);
-            top[k] = fmaxf(s[k >> 1][0][c], s[k >> 1][0][c + 1]);
+          for (int k = 0; k < 2 * NR; ++k) {
+            const int a = k >> 1, c = k & 1;
+            top[k] = fmaxf(s[0][a][c], s[0][a][2 + c]);
 #pragma unroll
-            for (int i = 1; i < HT; ++i) top[k] = max3(top[k], s[k >> 1][i][c], s[k >> 1][i][c + 1]);
-            grow |= top[k] > lim[k];
+            for (int i = 1; i < HT; ++i) top[k] = max3(top[k], s[i][a][c], s[i][a][2 + c]);
+            grow |= fmaf(top[k], scale[k], negm[k]) > LIFT + kRowsLazy;
           }
           if (__any_sync(0xffffffffu, grow)) {
+            unset = false;
 #pragma unroll
-            for (int k = 0; k < 2 * MT; ++k) {
+            for (int k = 0; k < 2 * NR; ++k) {
               float x = top[k];
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-              if (x > lim[k]) {   // (the same for the row's four lanes)
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+              const bool had = has >> k & 1u;
+              if (x != -INFINITY && (!had || fmaf(x, scale[k], negm[k]) > LIFT + kRowsLazy)) {   // (the same for the row's eight lanes)
                 const float to = LIFT - x * scale[k];
-                const float alpha = lim[k] == -INFINITY ? 1.f : fast_exp2(to - negm[k]);
-                lim[k] = x + kRowsLazy / scale[k];
+                const float alpha = had ? fast_exp2(to - negm[k]) : 1.f;
                 negm[k] = to;
+                has |= 1u << k;
                 l[k] *= alpha;
 #pragma unroll
                 for (int b = 0; b < NT; ++b) {
-                  o[k >> 1][b][2 * (k & 1)] *= alpha;
-                  o[k >> 1][b][2 * (k & 1) + 1] *= alpha;
+                  o[k >> 1][b][k & 1] *= alpha;
+                  o[k >> 1][b][2 + (k & 1)] *= alpha;
                 }
               }
             }
+            unset = __any_sync(0xffffffffu, has != (1u << 2 * NR) - 1u);
           }
-          uint32_t pw[MT][HT / 2][4];
+          uint32_t pw[HT][NR][2];
 #pragma unroll
-          for (int k = 0; k < 2 * MT; ++k)
+          for (int i = 0; i < HT; ++i)
 #pragma unroll
-            for (int i = 0; i < HT; ++i) {
-              const float a = fast_exp2(fmaf(s[k >> 1][i][2 * (k & 1)], scale[k], negm[k]));
-              const float b = fast_exp2(fmaf(s[k >> 1][i][2 * (k & 1) + 1], scale[k], negm[k]));
-              l[k] += a + b;
-              pw[k >> 1][i >> 1][(k & 1) + 2 * (i & 1)] = pack2_f16_sat(a, b);
-            }
-          // ---- O += P V, 16 positions at a time
+            for (int a = 0; a < NR; ++a)
 #pragma unroll
-          for (int hh = 0; hh < HT / 2; ++hh) {
-            uint32_t w[4][VW], sc[4];
+              for (int e = 0; e < 2; ++e) {
+                const float x = fast_exp2(fmaf(s[i][a][2 * e], scale[2 * a], negm[2 * a]));
+                const float y = fast_exp2(fmaf(s[i][a][2 * e + 1], scale[2 * a + 1], negm[2 * a + 1]));
+                l[2 * a] += x;
+                l[2 * a + 1] += y;
+                pw[i][a][e] = transpose8(pack2_f16_sat(x, y));   // rows by positions: row gi, positions 8 e + 2 t, + 1
+              }
+          // ---- O^T += V^T P^T, 16 positions at a time
+#pragma unroll
+          for (int i = 0; i < HT; ++i) {
+            uint32_t w[4][VW], sc[4];   // positions 2 t, 2 t + 1, 8 + 2 t, 9 + 2 t
 #pragma unroll
             for (int a = 0; a < 4; ++a) {
-              const int r = r0 + 16 * hh + 4 * a + t;
+              const int r = r0 + 16 * i + 4 * a + t;
               if constexpr (VW == 2) {
                 const uint2 v = *reinterpret_cast<const uint2*>(vb + r * (D / 2) + gi * 8);
                 w[a][0] = v.x; w[a][1] = v.y;
@@ -547,7 +586,7 @@ __global__ void __launch_bounds__(few_threads(D, MT), 1)
                 w[a][0] = *reinterpret_cast<const uint32_t*>(vb + r * (D / 2) + gi * 4);
                 sc[a] = vb[kSub * (D / 2) + r * (D / 16) + (gi >> 1)];
               }
-              if (masked && pos0 + 16 * hh + 4 * a + t >= len) {   // (zero weights times what lies there)
+              if (masked && pos0 + 16 * i + 4 * a + t >= len) {   // (zero weights times what lies there)
 #pragma unroll
                 for (int x = 0; x < VW; ++x) w[a][x] = 0;
                 sc[a] = 0;
@@ -561,15 +600,12 @@ __global__ void __launch_bounds__(few_threads(D, MT), 1)
               for (int a = 0; a < 4; ++a) e2m1x8_to_f16x8(w[a][x], v[a]);
 #pragma unroll
               for (int e = 0; e < 4; ++e) {   // dims 8 x + 2 e and the next of this lane's
-                const uint32_t b00 = mul_f16x2(__byte_perm(v[0][e], v[1][e], 0x5410), s01);
-                const uint32_t b01 = mul_f16x2(__byte_perm(v[2][e], v[3][e], 0x5410), s23);
-                const uint32_t b10 = mul_f16x2(__byte_perm(v[0][e], v[1][e], 0x7632), s01);
-                const uint32_t b11 = mul_f16x2(__byte_perm(v[2][e], v[3][e], 0x7632), s23);
+                const uint32_t fa[4] = {mul_f16x2(__byte_perm(v[0][e], v[1][e], 0x5410), s01),
+                                        mul_f16x2(__byte_perm(v[0][e], v[1][e], 0x7632), s01),
+                                        mul_f16x2(__byte_perm(v[2][e], v[3][e], 0x5410), s23),
+                                        mul_f16x2(__byte_perm(v[2][e], v[3][e], 0x7632), s23)};
 #pragma unroll
-                for (int a = 0; a < MT; ++a) {
-                  mma_f16(o[a][8 * x + 2 * e], pw[a][hh], b00, b01);
-                  mma_f16(o[a][8 * x + 2 * e + 1], pw[a][hh], b10, b11);
-                }
+                for (int a = 0; a < NR; ++a) mma_f16(o[a][4 * x + e], fa, pw[i][a][0], pw[i][a][1]);
               }
             }
           }
@@ -592,21 +628,16 @@ __global__ void __launch_bounds__(few_threads(D, MT), 1)
       // ------------------------------------------------------- end of the piece
       if (seq > 0 && !__all_sync(0xffffffffu, mbar_wait(mempty, static_cast<uint32_t>(seq - 1) & 1u, wt))) break;
 #pragma unroll
-      for (int k = 0; k < 2 * MT; ++k) {
-        const int r = gi + 8 * k;
-        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 1);
-        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 2);
-        if (t == 0) xml[warp * 16 * MT + r] = make_float2(-negm[k], l[k]);
-        // column 2 t + c of n-tile b is dim (D / 8) (2 t + c) + b
-        float4* row = share + (warp * 16 * MT + r) * (D / 4);
+      for (int k = 0; k < 2 * NR; ++k) {
+        const int a = k >> 1, c = k & 1, r = 8 * a + 2 * t + c;
+        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 4);
+        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 8);
+        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 16);
+        if (gi == 0) xml[warp * ROWS + r] = make_float2(-negm[k], l[k]);
+        float4* row = share + (warp * ROWS + r) * (D / 4);
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int b = 0; b < NT; b += 4) {
-            const int e = 2 * (k & 1) + c;
-            row[swz(r, (2 * t + c) * (D / 32) + b / 4)] =
-                make_float4(o[k >> 1][b][e], o[k >> 1][b + 1][e], o[k >> 1][b + 2][e], o[k >> 1][b + 3][e]);
-          }
+        for (int b = 0; b < NT; b += 2)
+          row[swz(r, gi * (D / 32) + b / 2)] = make_float4(o[a][b][c], o[a][b][2 + c], o[a][b + 1][c], o[a][b + 1][2 + c]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(mfull);

@@ -163,7 +163,7 @@ bool few_smem(const trtv_geom* g, const RowsPlan& pl, RowsAttnParams* p, size_t*
   const size_t page = 2 * static_cast<size_t>(kGroups) * kFp4Row * g->head_dim;
   const size_t scan = align_up((static_cast<size_t>(g->batch) + 1 + 32) * sizeof(int64_t), 16);
   const size_t q = align_up(2 * static_cast<size_t>(f.q_bytes), 128);
-  const size_t rows = static_cast<size_t>(f.consumers) * 8 * pl.few, share = rows * g->head_dim * sizeof(float), ml = rows * 2 * sizeof(float);
+  const size_t rows = static_cast<size_t>(f.consumers) * 8 * pl.few, share = rows * g->head_dim * sizeof(float), ml = rows * 3 * sizeof(float);
   const size_t pieces = 4 * 48, bars = (2 * kFewStages + 16) * sizeof(uint64_t);
   const size_t fixed = q + share + ml + pieces + scan + bars + kAlignSlack;
   // (whole sets: a stage's pages are then always the same warps', whose parities cannot fall two phases behind)

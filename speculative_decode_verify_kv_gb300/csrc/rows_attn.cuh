@@ -487,7 +487,10 @@ __global__ void __launch_bounds__(KV != TRTV_BF16 ? 512 : 384, 1)
   const RowsGeom& g = p.g;
 
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  // (E2M1 prompts: through a shared address, so that the compiler sees whose loads and stores these are: 4 chunks over
+  // 2-12 k positions 139.8 -> 132.0 us; one-tile items keep the other form, 102 us against 107)
+  uint8_t* smem = FP4 && TWO ? static_cast<uint8_t*>(__cvta_shared_to_generic((smem_u32(smem_raw) + 1023) & ~1023u))
+                             : reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const int NST = p.nst, NRAW = p.nraw;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.off_bar);  // [NST] page ready for the UMMAs
   uint64_t* empty = full + NST;                                    // [NST] UMMAs done with it

@@ -23,7 +23,7 @@ cudaError_t launch_rows_few(int head_dim, int nr, const CUtensorMap& kv_map, con
 }
 
 FewShape few_shape(int head_dim, int nr) {
-  return {few_warps(nr), few_q_bytes(head_dim, nr), few_warps(nr) * few_tiles(nr) * 16 / kPage};
+  return {few_warps(nr), few_q_bytes(head_dim, nr), few_warps(nr) * few_tiles(head_dim, nr) * 16 / kPage};
 }
 
 }  // namespace trtv

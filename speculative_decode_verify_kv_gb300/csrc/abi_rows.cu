@@ -27,7 +27,12 @@ constexpr float kMinScale = 5.421011e-20f;  // 2^-64
 // 700-1500 17.0 / 15.6 / 16.1.  E4M3, at 64 / 128 / 256 / 384: 64 trees 113.1 / 110.8 /
 // 105.8 / 100.7, one over 700 14.4 / 14.5 / 15.0 / 14.4, one over 16000 30.0 at each.
 constexpr int kRowsSetupTwo = 256, kRowsSetupTwoFp8 = 512, kRowsSetupOne = 128, kRowsSetupOneFp8 = 256;
-constexpr int kFewSetup = 256;
+// E2M1 caches.  One tile, at 128 / 256 / 384 / 512: 64 trees of 16 nodes 105.5 / 102.3 / 99.0 / 96.4, 32 requests of 64
+// rows 85.1 / 81.0 / 77.5 / 76.9, one tree of 8 over 900 15.9 / 17.3 / 16.3 / 16.4 (256-row items as E4M3: 4 chunks at 256 /
+// 512 / 768 / 1024 134.9 / 130.9 / 131.0 / 134.3).  Few rows, at 128 / 256 / 512 / 768: 64 requests of 8 rows 42.1 / 40.7 / 40.5 /
+// 41.4, of 32 rows 91.3 / 89.0 / 86.2 / 88.3, 256 of 100-1500 positions 58.6 / 53.5 / 49.3 / 46.9, 16 with 8 KV heads 28.0 /
+// 28.0 / 28.7 / 29.4.
+constexpr int kRowsSetupOneFp4 = 512, kFewSetup = 512;
 
 // Geometry checks shared by the packed-row calls.
 trtv_status rows_geom(const trtv_geom* g, const int32_t* indptr, int32_t num_tokens, RowsGeom* r) {
@@ -266,7 +271,11 @@ trtv_status rows_attn(const trtv_geom* g, const void* q, const void* pool, const
   p.out_f32 = out_dtype == TRTV_F32;
   p.num_ctas = pl.num_ctas;
   const bool codes = g->kv_dtype != TRTV_BF16;
-  p.setup = pl.few > 0 ? kFewSetup : pl.two ? (codes ? kRowsSetupTwoFp8 : kRowsSetupTwo) : codes ? kRowsSetupOneFp8 : kRowsSetupOne;
+  p.setup = pl.few > 0 ? kFewSetup
+            : pl.two   ? (codes ? kRowsSetupTwoFp8 : kRowsSetupTwo)
+            : fp4      ? kRowsSetupOneFp4
+            : codes    ? kRowsSetupOneFp8
+                       : kRowsSetupOne;
   p.scale_log2 = g->sm_scale * g->k_scale * 1.4426950408889634f;
   p.v_scale = g->v_scale;
   p.wait_ns = wait_limit_ns();

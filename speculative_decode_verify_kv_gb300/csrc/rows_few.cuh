@@ -416,13 +416,13 @@ __global__ void __launch_bounds__(few_threads(NR), 1)
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) q[a][i] = frag[(a * (D / 32) + i) * 32];
       }
-      // rows of this lane: 8 a + 2 t + c, at k = 2 a + c; negm: LIFT - maximum scale
-      float scale[2 * NR], negm[2 * NR], l[2 * NR];
+      // rows of this lane: 8 a + 2 t + c, c the two of a pair; negm: LIFT - maximum scale
+      float2 scale[NR], negm[NR], l[NR];
 #pragma unroll
-      for (int k = 0; k < 2 * NR; ++k) {
-        scale[k] = qscale[8 * (k >> 1) + 2 * t + (k & 1)];
-        negm[k] = LIFT;
-        l[k] = 0.f;
+      for (int a = 0; a < NR; ++a) {
+        scale[a] = *reinterpret_cast<const float2*>(qscale + 8 * a + 2 * t);
+        negm[a] = make_float2(LIFT, LIFT);
+        l[a] = make_float2(0.f, 0.f);
       }
       bool unset = true;   // some row has no maximum yet (its negm is LIFT)
       uint32_t has = 0;    // rows that have one
@@ -526,36 +526,44 @@ __global__ void __launch_bounds__(few_threads(NR), 1)
                 }
             }
           }
-          // ---- weights
-          bool grow = unset;
-          float top[2 * NR];
+          // ---- weights: 2^(logit - maximum), lifted
+          float top = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 2 * NR; ++k) {
-            const int a = k >> 1, c = k & 1;
-            top[k] = fmaxf(s[0][a][c], s[0][a][2 + c]);
+          for (int i = 0; i < HT; ++i)
 #pragma unroll
-            for (int i = 1; i < HT; ++i) top[k] = max3(top[k], s[i][a][c], s[i][a][2 + c]);
-            grow |= fmaf(top[k], scale[k], negm[k]) > LIFT + kRowsLazy;
-          }
-          if (__any_sync(0xffffffffu, grow)) {
-            unset = false;
+            for (int a = 0; a < NR; ++a)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float2 v = __ffma2_rn(make_float2(s[i][a][2 * e], s[i][a][2 * e + 1]), scale[a], negm[a]);
+                s[i][a][2 * e] = v.x;
+                s[i][a][2 * e + 1] = v.y;
+                top = max3(top, v.x, v.y);
+              }
+          if (__any_sync(0xffffffffu, unset || top > LIFT + kRowsLazy)) {
 #pragma unroll
             for (int k = 0; k < 2 * NR; ++k) {
-              float x = top[k];
+              const int a = k >> 1, c = k & 1;
+              float x = fmaxf(s[0][a][c], s[0][a][2 + c]);
+#pragma unroll
+              for (int i = 1; i < HT; ++i) x = max3(x, s[i][a][c], s[i][a][2 + c]);
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
               x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
               const bool had = has >> k & 1u;
-              if (x != -INFINITY && (!had || fmaf(x, scale[k], negm[k]) > LIFT + kRowsLazy)) {   // (the same for the row's eight lanes)
-                const float to = LIFT - x * scale[k];
-                const float alpha = had ? fast_exp2(to - negm[k]) : 1.f;
-                negm[k] = to;
+              if (x != -INFINITY && (!had || x > LIFT + kRowsLazy)) {   // (the same for the row's eight lanes)
+                const float shift = LIFT - x, alpha = had ? fast_exp2(shift) : 1.f;
+                (c ? negm[a].y : negm[a].x) += shift;
+                (c ? l[a].y : l[a].x) *= alpha;
                 has |= 1u << k;
-                l[k] *= alpha;
 #pragma unroll
                 for (int b = 0; b < NT; ++b) {
-                  o[k >> 1][b][k & 1] *= alpha;
-                  o[k >> 1][b][2 + (k & 1)] *= alpha;
+                  o[a][b][c] *= alpha;
+                  o[a][b][2 + c] *= alpha;
+                }
+#pragma unroll
+                for (int i = 0; i < HT; ++i) {
+                  s[i][a][c] += shift;
+                  s[i][a][2 + c] += shift;
                 }
               }
             }
@@ -568,11 +576,9 @@ __global__ void __launch_bounds__(few_threads(NR), 1)
             for (int a = 0; a < NR; ++a)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const float x = fast_exp2(fmaf(s[i][a][2 * e], scale[2 * a], negm[2 * a]));
-                const float y = fast_exp2(fmaf(s[i][a][2 * e + 1], scale[2 * a + 1], negm[2 * a + 1]));
-                l[2 * a] += x;
-                l[2 * a + 1] += y;
-                pw[i][a][e] = transpose8(pack2_f16_sat(x, y));   // rows by positions: row gi, positions 8 e + 2 t, + 1
+                const float2 v = make_float2(fast_exp2(s[i][a][2 * e]), fast_exp2(s[i][a][2 * e + 1]));
+                l[a] = __fadd2_rn(l[a], v);
+                pw[i][a][e] = transpose8(pack2_f16_sat(v.x, v.y));   // rows by positions: row gi, positions 8 e + 2 t, + 1
               }
           // ---- O^T += V^T P^T, 16 positions at a time
 #pragma unroll
@@ -633,10 +639,11 @@ __global__ void __launch_bounds__(few_threads(NR), 1)
 #pragma unroll
       for (int k = 0; k < 2 * NR; ++k) {
         const int a = k >> 1, c = k & 1, r = 8 * a + 2 * t + c;
-        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 4);
-        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 8);
-        l[k] += __shfl_xor_sync(0xffffffffu, l[k], 16);
-        if (gi == 0) xml[warp * ROWS + r] = make_float2(-negm[k], l[k]);
+        float sum = c ? l[a].y : l[a].x;
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        if (gi == 0) xml[warp * ROWS + r] = make_float2(-(c ? negm[a].y : negm[a].x), sum);
         float4* row = share + (warp * ROWS + r) * (D / 4);
 #pragma unroll
         for (int b = 0; b < NT; b += 2)

@@ -69,7 +69,7 @@ __device__ __forceinline__ uint32_t pack8_e2m1(const float (&t)[8], float s) {
 }
 
 template <int D, int KV, bool INTER>
-__global__ void __launch_bounds__(kStageThreads, KV == TRTV_FP4_E2M1 ? 8 : 1) norm_rope_stage_kernel(const __grid_constant__ NormRopeParams p) {
+__global__ void __launch_bounds__(kStageThreads, KV == TRTV_FP4_E2M1 ? 8 : 7) norm_rope_stage_kernel(const __grid_constant__ NormRopeParams p) {
   constexpr bool FP8 = KV == TRTV_FP8_E4M3, FP4 = KV == TRTV_FP4_E2M1;
   // E2M1: a head's values change lanes here, so that two neighbours hold 16 dims in order
   __shared__ __align__(16) float swap[FP4 ? kStageThreads / 32 : 1][FP4 ? 32 * 8 : 1];

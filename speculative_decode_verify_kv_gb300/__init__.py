@@ -31,7 +31,7 @@ TRTV_OK, TRTV_ERR_INVALID_ARG, TRTV_ERR_UNSUPPORTED, TRTV_ERR_CUDA, TRTV_ERR_WOR
 TRTV_BF16, TRTV_FP8_E4M3, TRTV_F32, TRTV_FP4_E2M1 = 0, 1, 2, 3
 DEVERR_KV_LEN, DEVERR_PAGE_ID, DEVERR_BLOCK_IDX, DEVERR_TIMEOUT = 1, 2, 4, 8
 DEVERR_INDPTR, DEVERR_POSITION, DEVERR_PATH = 16, 32, 64
-DEVERR_SLOTS, DEVERR_REFS, DEVERR_PARENT = 128, 256, 512
+DEVERR_SLOTS, DEVERR_REFS, DEVERR_PARENT, DEVERR_LOGITS = 128, 256, 512, 1024
 
 # every function the C header declares
 EXPORTS = ("trtv_status_string", "trtv_version", "trtv_subpage_view", "trtv_workspace_bytes",

@@ -352,6 +352,7 @@ __global__ void __launch_bounds__(few_threads(NR), 1)
 #pragma unroll
           for (int w = 0; w < CW; w += 4)
             *reinterpret_cast<float4*>(fac + r * CW + w) = make_float4(x[w].x * f, x[w + 1].x * f, x[w + 2].x * f, x[w + 3].x * f);
+          report_far(g.err, top);
           if (!whole) p.ws_lse[slot * ROWS + r] = lt == 0.f ? -INFINITY : top + __log2f(lt);
         }
         __syncwarp();

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional
 
 from . import _build
@@ -68,6 +69,9 @@ class NormRope(ctypes.Structure):
                 ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("rope_table", ctypes.c_void_p),
                 ("positions", ctypes.c_void_p), ("table_len", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
                 ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+_NORM_ROPE = struct.Struct("=QQQqqqQQQQiiif")
 
 
 _lib: Optional[ctypes.CDLL] = None
@@ -165,8 +169,7 @@ def _ptr(x) -> int:
 
 def _stream(stream) -> int:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _begin(None)[1]
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -325,7 +328,7 @@ def _begin(stream):
         import torch
         torch.cuda.init()
         _torch = torch
-    dev = _torch.cuda.current_device()
+    dev = _torch._C._cuda_getDevice()
     if stream is None:
         return dev, _torch._C._cuda_getCurrentRawStream(dev)
     return dev, stream if isinstance(stream, int) else stream.cuda_stream
@@ -394,12 +397,13 @@ def trtv_norm_rope_stage(geom: Geom, q, k, v, q_weight, k_weight, eps: float, ro
     kp, k_pitch = _rows_arg(fn, "k", k, dev, ks)
     vp, v_pitch = _rows_arg(fn, "v", v, dev, ks)
     table_len = 0 if rope_table is None else rope_table.shape[0]
-    a = NormRope(qp, kp, vp, q_pitch, k_pitch, v_pitch,
-                 None if q_weight is None else _arg(fn, "q_weight", q_weight, dev, bf16, (d,)),
-                 None if k_weight is None else _arg(fn, "k_weight", k_weight, dev, bf16, (d,)),
-                 None if rope_table is None else _arg(fn, "rope_table", rope_table, dev, _torch.float32, (table_len, rot_dim)),
-                 None if positions is None else _arg(fn, "positions", positions, dev, _torch.int32, (rows,)),
-                 table_len, rot_dim, 1 if interleaved else 0, eps)
+    a = NormRope.from_buffer_copy(_NORM_ROPE.pack(   # (0.5 us less than naming the fields)
+        qp, kp, vp, q_pitch, k_pitch, v_pitch,
+        0 if q_weight is None else _arg(fn, "q_weight", q_weight, dev, bf16, (d,)),
+        0 if k_weight is None else _arg(fn, "k_weight", k_weight, dev, bf16, (d,)),
+        0 if rope_table is None else _arg(fn, "rope_table", rope_table, dev, _torch.float32, (table_len, rot_dim)),
+        0 if positions is None else _arg(fn, "positions", positions, dev, _torch.int32, (rows,)),
+        table_len, rot_dim, 1 if interleaved else 0, eps))
     pt, kl, ip = _tables(fn, geom, page_table, kv_lens, qo_indptr, dev)
     _check(fn, load().trtv_norm_rope_stage(ctypes.byref(geom), ctypes.byref(a), ip, rows,
                                            _arg(fn, "q_out", q_out, dev, bf16, qs), _pool_arg(fn, geom, kv_pool, dev),

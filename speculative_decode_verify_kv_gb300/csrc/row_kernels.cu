@@ -49,13 +49,6 @@ __device__ __forceinline__ uint32_t pack4_e4m3(const float (&x)[4], float scale)
   return lo | (hi << 16);
 }
 
-// max that keeps a NaN
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
 // Eight E2M1 codes of t / s, nearest even, saturated to +-6, the first in the lowest bits.
 __device__ __forceinline__ uint32_t pack8_e2m1(const float (&t)[8], float s) {
   uint32_t r;

@@ -132,6 +132,13 @@ __device__ __forceinline__ int64_t fp4_block(const RowsGeom& g, int64_t s, int p
   return (s * g.slot_stride * kGroups + (pos % kPage) / kSub) * g.num_kv_heads * static_cast<int64_t>(kFp4Row * D);
 }
 
+// max that keeps a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // four E4M3 codes' pairs and eight E2M1 codes -> f16 (exact), and a product of f16 pairs
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2_reg(uint32_t two) {
   uint32_t r;

@@ -19,13 +19,16 @@ cudaError_t launch_rows_attn_fp8(bool two, const CUtensorMap& kv_map, const CUte
 // `cont` word (no ranges are computed here).  Nothing past the last piece is
 // loaded (items of two pieces, 4 chunks of 300-512 tokens: 120.5 -> 117 us).  Batches
 // of two, six CTAs an SM: 115 us, but a tree cut into many pieces 16.5 -> 18.3.
+// Few rows (E2M1): up to eight pieces at a time, their weights side by side, two CTAs
+// an SM for the registers (one request's decoding over 8000 positions, head_dim 128,
+// 16.7 -> 14.8 us, over 60000 23.0 -> 21.3; twelve at a time 15.2 and 22.2).
 constexpr int kJoinThreads = 256;
 constexpr int kJoinRows = 16;   // (or all of a piece with fewer)
 
 template <int D, int ROWS>
-__global__ void __launch_bounds__(kJoinThreads, 4) rows_join_kernel(const __grid_constant__ RowsAttnParams p) {
+__global__ void __launch_bounds__(kJoinThreads, ROWS > 32 ? 4 : 2) rows_join_kernel(const __grid_constant__ RowsAttnParams p) {
   constexpr int JR = ROWS < kJoinRows ? ROWS : kJoinRows;
-  constexpr int F4 = D / 4, EL = (JR * F4 + kJoinThreads - 1) / kJoinThreads, kBatch = 4;
+  constexpr int F4 = D / 4, EL = (JR * F4 + kJoinThreads - 1) / kJoinThreads, kBatch = ROWS > 32 ? 4 : EL == 1 ? 8 : 4;
   const RowsGeom& g = p.g;
   const int c0 = blockIdx.x / (ROWS / JR), chunk = blockIdx.x % (ROWS / JR), tid = threadIdx.x;
   pdl_wait();
@@ -67,6 +70,30 @@ __global__ void __launch_bounds__(kJoinThreads, 4) rows_join_kernel(const __grid
     }
 #pragma unroll
     for (int u = 0; u < EL; ++u) {
+      if constexpr (ROWS <= 32) {   // (the pieces' weights side by side, not one after the other)
+        float mn = m[u];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          if (used[k]) mn = max_nan(mn, x[u][k]);
+        if (mn == -INFINITY) continue;
+        const float so = exp2f(m[u] - mn);
+        float w[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) w[k] = used[k] ? exp2f(x[u][k] - mn) : 0.f;
+        l[u] *= so;
+        acc[u] = make_float4(acc[u].x * so, acc[u].y * so, acc[u].z * so, acc[u].w * so);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+          if (w[k] == 0.f) continue;   // (what lies there may be anything)
+          l[u] += w[k];
+          acc[u].x += w[k] * v[u][k].x;
+          acc[u].y += w[k] * v[u][k].y;
+          acc[u].z += w[k] * v[u][k].z;
+          acc[u].w += w[k] * v[u][k].w;
+        }
+        m[u] = mn;
+        continue;
+      }
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         if (!used[k] || x[u][k] == -INFINITY) continue;

@@ -40,7 +40,15 @@
 // deviation of 6 (a prompt of 16384), 2206 so.
 //
 // E2M1 caches: the same, a code times its block's E4M3 scale being exact in f16
-// (at most 6 significant bits, magnitudes 2^-10 .. 2688).
+// (at most 6 significant bits, magnitudes 2^-10 .. 2688).  A page of K or V is one
+// tensor load (a bulk copy per group, 8 a page, is issued one after the other: a
+// verify step of 8 requests of 128 rows a head over 131 k positions 327 -> 266 us).
+// That step takes 263 us (1.04 PFLOP/s), 64 trees of 16 nodes 96, 4 chunks over
+// 2-12 k positions 133, a prompt of 16384 1470.  With the conversion left out of a
+// scratch copy, waits and arrivals kept, 246, 93, 131 and 1447: a tile's chain and
+// shared memory bound it (QK reads Q and K from it for 512 cycles, a page's tiles
+// are written in 512 and V read in 256, of 2150).  Two issuers for one-tile items,
+// each group with stages of its own, in turns or not: 281 and 104-109.
 //
 // What bounds a prompt's page is one group's chain: softmax, then PV and the
 // next QK, which cannot start before P is written over S.  So a row's scores are

@@ -29,6 +29,17 @@
 // fragments.  So a piece costs the consumers little more than its pages (joined
 // by all warps at a barrier, with Q loaded by each: 5.4 us a piece against 0.6 a
 // page).
+//
+// Measured, K/V bytes over time (head_dim 128, 4 KV heads): 64 requests of 1-8 k
+// positions, 8 rows a head 40.2 us (156 MB, 58 % of the copy rate: the pages arrive
+// at the full rate, start, split ends and join are 15 of the 40), 16 rows 50.4, 32
+// rows 84.6 (the matrix instructions alone 32, conversion 20, softmax 10); 256
+// requests of 100-1500 50; one request over 60000 positions 21.4, over 8000 14.7.
+// One tile of rows_attn.cuh for each: 99, 97 and 98 us for 8, 16 and 32 rows.
+// Tried: K in tensor memory with tcgen05 and P V here (32 rows 109), all of it on
+// tcgen05 with positions as M (116 for 64 trees of 16 nodes), 16 warps with half the
+// rows each (109), a page of discarded work before the first piece, to have the
+// loop's instructions near (0.7 us slower).
 // Work split, pieces, the join between CTAs and the refusals are rows_attn.cuh's,
 // with one item per (request, KV head).
 #pragma once

@@ -70,22 +70,20 @@ __device__ __forceinline__ I block_before(I x, I* tot, I& all) {
   return before;
 }
 
-// Exclusive sums of n counts into pre[0 .. n], capped so that they cannot pass 2^30.
-template <typename F>
-__device__ __forceinline__ int block_sums(int n, int* pre, int64_t* tot, F count) {
-  constexpr int64_t kCap = 1 << 30;
+// Exclusive sums of n counts, put(0 .. n, sum); returns the last.
+template <typename F, typename P>
+__device__ __forceinline__ int64_t block_sums(int n, int64_t* tot, F count, P put) {
   int64_t run = 0;
   for (int i0 = 0; i0 < n; i0 += kPagesThreads) {
     const int i = i0 + threadIdx.x;
     int64_t all;
-    const int64_t before = block_before(static_cast<int64_t>(i < n ? count(i) : 0), tot, all);
-    if (i < n) pre[i] = static_cast<int>(min(kCap, run + before));
+    const int64_t before = block_before(i < n ? count(i) : int64_t{0}, tot, all);
+    if (i < n) put(i, run + before);
     run += all;
   }
-  run = min(kCap, run);
-  if (threadIdx.x == 0) pre[n] = static_cast<int>(run);
+  if (threadIdx.x == 0) put(n, run);
   __syncthreads();
-  return static_cast<int>(run);
+  return run;
 }
 
 // The largest i in [0, n) with pre[i] <= k: k lies in its share when k < pre[n]
@@ -236,15 +234,12 @@ size_t pages_smem(int chunks, int new_batch) { return (static_cast<size_t>(chunk
 
 namespace {
 
-// All bits that the scan found, for the whole CTA.
-__device__ __forceinline__ int found_bad(const PagesParams& p, int* word) {
-  if (threadIdx.x == 0) *word = 0;
-  __syncthreads();
+// Whether the scan found an error, for the whole CTA; CTA 0 reports it.
+__device__ __forceinline__ bool found_bad(const PagesParams& p) {
   int bad = 0;
   for (int i = threadIdx.x; i < p.chunks + p.g.batch + p.new_batch; i += kPagesThreads) bad |= p.ws.bad[i];
-  if (bad != 0) atomicOr(word, bad);
-  __syncthreads();
-  return *word;
+  if (blockIdx.x == 0 && bad != 0) atomicOr(p.g.err, bad);
+  return __syncthreads_or(bad) != 0;
 }
 
 __device__ __forceinline__ int chunk_slots(const PagesParams& p, int i) { return min(kSlotChunk, p.g.num_slots - i * kSlotChunk); }
@@ -259,7 +254,6 @@ __device__ __forceinline__ int chunk_slots(const PagesParams& p, int i) { return
 __global__ void __launch_bounds__(kPagesThreads, kForkCtas) pages_fork_kernel(const __grid_constant__ PagesParams p) {
   extern __shared__ int sums[];
   __shared__ int64_t tot[kPagesThreads / 32];
-  __shared__ int word;
   const RowsGeom& g = p.g;
   const int tid = threadIdx.x, lane = tid & 31, N = p.new_batch;
   int* const slots = sums;                 // [chunks + 1] free slots before each chunk
@@ -267,22 +261,29 @@ __global__ void __launch_bounds__(kPagesThreads, kForkCtas) pages_fork_kernel(co
   int* const copies = fresh + N + 1;       // [N + 1] copied pages before it
   pdl_wait();
   pdl_trigger();
-  int bad = found_bad(p, &word);
-  if (bad == 0) {
-    const int have = block_sums(p.chunks, slots, tot, [&](int i) { return p.ws.free[i]; });
-    const int want = block_sums(N, fresh, tot, [&](int i) { return p.ws.child[i].x; });
-    if (want > have) bad = TRTV_DEVERR_SLOTS;
-  }
-  if (bad != 0) {
-    if (blockIdx.x == 0 && tid == 0) atomicOr(g.err, bad);
+  if (found_bad(p)) return;
+  auto parent_len = [&](int c) { return p.parent[c] >= 0 ? g.kv_lens[p.parent[c]] : 0; };
+  const int have = static_cast<int>(block_sums(
+      p.chunks, tot, [&](int i) { return static_cast<int64_t>(p.ws.free[i]); }, [&](int i, int64_t v) { slots[i] = static_cast<int>(v); }));
+  // both sums of the new requests at once: fresh slots (at most 2^34) below, copied pages above
+  constexpr int kLow = 40;
+  constexpr int64_t kMask = (int64_t{1} << kLow) - 1, kCap = 1 << 30;
+  const int64_t both = block_sums(
+      N, tot,
+      [&](int c) {
+        const int len = parent_len(c);
+        const int2 x = p.ws.child[c];
+        return static_cast<int64_t>(x.x) | (x.x > 0 && x.y == len / kPage && len % kPage != 0 ? int64_t{1} << kLow : 0);
+      },
+      [&](int c, int64_t v) {
+        fresh[c] = static_cast<int>(min(kCap, v & kMask));   // (past the free slots: not used)
+        copies[c] = static_cast<int>(v >> kLow);
+      });
+  const int ncopies = static_cast<int>(both >> kLow);
+  if ((both & kMask) > have) {
+    if (blockIdx.x == 0 && tid == 0) atomicOr(g.err, TRTV_DEVERR_SLOTS);
     return;
   }
-  auto parent_len = [&](int c) { return p.parent[c] >= 0 ? g.kv_lens[p.parent[c]] : 0; };
-  const int ncopies = block_sums(N, copies, tot, [&](int c) {
-    const int len = parent_len(c);
-    const int2 x = p.ws.child[c];
-    return x.x > 0 && x.y == len / kPage && len % kPage != 0 ? 1 : 0;
-  });
   auto slot_of = [&](int k) {
     const int i = share_of(slots, p.chunks, k);
     return p.ws.list[i * kSlotChunk + k - slots[i]];
@@ -354,18 +355,14 @@ constexpr int kMoveBytes = 8192;   // that a warp copies at a time
 __global__ void __launch_bounds__(kPagesThreads) pages_compact_kernel(const __grid_constant__ PagesParams p) {
   extern __shared__ int sums[];
   __shared__ int64_t tot[kPagesThreads / 32];
-  __shared__ int word;
   const RowsGeom& g = p.g;
   const int tid = threadIdx.x, lane = tid & 31;
   int* const slots = sums;   // [chunks + 1] free slots before each chunk
   pdl_wait();
   pdl_trigger();
-  const int bad = found_bad(p, &word);
-  if (bad != 0) {
-    if (blockIdx.x == 0 && tid == 0) atomicOr(g.err, bad);
-    return;
-  }
-  const int nfree = block_sums(p.chunks, slots, tot, [&](int i) { return p.ws.free[i]; });
+  if (found_bad(p)) return;
+  const int nfree = static_cast<int>(block_sums(
+      p.chunks, tot, [&](int i) { return static_cast<int64_t>(p.ws.free[i]); }, [&](int i, int64_t v) { slots[i] = static_cast<int>(v); }));
   const int U = g.num_slots - nfree;
   // free slots below U: those of the chunks before U's, and some of its own
   const int cu = U / kSlotChunk;

@@ -62,6 +62,21 @@ def test_largest_batches(batch, n, hq, d):
     check(p, p.dense())
 
 
+@pytest.mark.parametrize("kind,d", [("prompt", 128), ("prompt", 64), ("tree", 128), ("tree", 64)])
+def test_largest_batches_of_tiles(kind, d):
+    """The same beside 256-row items (some requests have many tokens) and 128-row items."""
+    most = 300 if kind == "prompt" else 20
+    new = [most if i % 211 == 0 else i % 3 for i in range(2048)]
+    p = Fp4Rows(new, [(i * 37) % 170 if i % 97 else 1200 for i in range(2048)], 4, 1, d, pad=1, seed=d)
+    v = p.values()
+    p.values = lambda pool=None: v
+    if kind == "prompt":
+        check(p, p.prompt())
+    else:
+        m = p.tree_masks()
+        check(p, p.tree(m), m)
+
+
 @pytest.mark.parametrize("hq,n", [(32, 1), (32, 4), (32, 20)])
 def test_slots_past_four_gigabytes(hq, n):
     """The same pages at the start of a small pool and at the end of one of 5.9 GB."""

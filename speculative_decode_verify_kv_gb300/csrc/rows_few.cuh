@@ -33,8 +33,8 @@
 // Measured, K/V bytes over time (head_dim 128, 4 KV heads): 64 requests of 1-8 k
 // positions, 8 rows a head 40.2 us (156 MB, 58 % of the copy rate: the pages arrive
 // at the full rate, start, split ends and join are 15 of the 40), 16 rows 50.4, 32
-// rows 84.6 (the matrix instructions alone 32, conversion 20, softmax 10); 256
-// requests of 100-1500 50; one request over 60000 positions 21.4, over 8000 14.7.
+// rows 78.7 (the matrix instructions alone 32, conversion 20, softmax 10); 256
+// requests of 100-1500 49; one request over 60000 positions 21.4, over 8000 14.7.
 // One tile of rows_attn.cuh for each: 99, 97 and 98 us for 8, 16 and 32 rows.
 // Tried: K in tensor memory with tcgen05 and P V here (32 rows 109), all of it on
 // tcgen05 with positions as M (116 for 64 trees of 16 nodes), 16 warps with half the
@@ -55,16 +55,20 @@ constexpr int align16(int x) { return (x + 15) / 16 * 16; }
 
 // Consumer warps, in whole warpgroups, the registers of a thread of theirs and of
 // the other four warps, tiles of 16 positions that a warp takes at a time, and
-// whether Q's fragments stay in its registers.
+// whether Q's fragments stay in its registers.  Consumers and others, head_dim 128, 32
+// rows, 64 requests: 208 and 88 registers 92.2 us, 216 and 72 90.0, 224 and 56 84.6,
+// 232 and 40 80.1, with the merging loop not unrolled 78.7 (one request over 900
+// positions 17.0 -> 17.5); 16 rows, 152 and 56 50.3, 144 and 80 51.6; 8 rows, 256 short
+// requests, 104 and 56 49.7, 104 and 64 48.9.
 constexpr int few_warps(int NR) { return NR == 1 ? 16 : NR == 2 ? 12 : 8; }
-constexpr int few_regs(int NR) { return NR == 1 ? 104 : NR == 2 ? 152 : 224; }
-constexpr int kFewOtherRegs = 56;
+constexpr int few_regs(int D, int NR) { return NR == 1 ? 104 : NR == 2 ? 152 : D == 128 ? 232 : 216; }
+constexpr int few_other_regs(int D, int NR) { return NR == 1 ? 64 : NR == 2 ? 56 : D == 128 ? 40 : 72; }
 constexpr int few_tiles(int D, int NR) { return NR == 4 && D == 128 ? 1 : 2; }
 constexpr bool few_q_regs(int NR) { return NR == 1; }
 constexpr int few_threads(int NR) { return 32 * few_warps(NR) + 128; }
 constexpr int few_q_bytes(int D, int NR) { return NR * (D / 32) * 512 + align16(NR * 32); }   // fragments and scales of a piece
-constexpr bool few_registers_fit(int NR) {   // setmaxnreg draws on what the block was launched with
-  return 32 * few_warps(NR) * few_regs(NR) + 128 * kFewOtherRegs <= few_threads(NR) * (65536 / few_threads(NR) / 8 * 8);
+constexpr bool few_registers_fit(int D, int NR) {   // setmaxnreg draws on what the block was launched with
+  return 32 * few_warps(NR) * few_regs(D, NR) + 128 * few_other_regs(D, NR) <= few_threads(NR) * (65536 / few_threads(NR) / 8 * 8);
 }
 
 // (not volatile: the compiler may move it among what it does not depend on)
@@ -102,9 +106,10 @@ __global__ void __launch_bounds__(few_threads(NR), 1)
   constexpr int UPP = kPage / (16 * HT);       // of which a page has
   constexpr int SETS = CW / UPP;               // pages at a time
   constexpr bool QREG = few_q_regs(NR);
+  constexpr bool LEAN = few_other_regs(D, NR) < 56;   // few registers beside the consumers
   constexpr int QB = few_q_bytes(D, NR), QSCALE = NR * (D / 32) * 512;
   static_assert(CW % UPP == 0, "whole pages");
-  static_assert(few_registers_fit(NR), "registers");
+  static_assert(few_registers_fit(D, NR), "registers");
   const RowsGeom& g = p.g;
 
   extern __shared__ uint8_t smem_raw[];
@@ -167,7 +172,7 @@ __global__ void __launch_bounds__(few_threads(NR), 1)
     }
   } else if (warp >= CW) {
     // ------------------------------------------------------------ producers
-    set_registers<kFewOtherRegs, false>();
+    set_registers<few_other_regs(D, NR), false>();
     if (warp == CW) {
       // page loads
       const uint64_t pol = policy_evict_first();
@@ -281,8 +286,8 @@ __global__ void __launch_bounds__(few_threads(NR), 1)
         const int gi = lane >> 2, t = lane & 3;
         uint4* frag = reinterpret_cast<uint4*>(qbuf + sl * QB);
         float* qscale = reinterpret_cast<float*>(qbuf + sl * QB + QSCALE);
-        uint4 w[NR <= 2 ? NR : 2][D / 32];
         constexpr int AT = NR <= 2 ? NR : 2;   // tiles of rows at a time
+        uint4 w[AT][D / 32];
 #pragma unroll 1
         for (int a0 = 0; a0 < NR; a0 += AT) {
 #pragma unroll
@@ -369,7 +374,7 @@ __global__ void __launch_bounds__(few_threads(NR), 1)
         }
         __syncwarp();
         // (a consumer without weight for a row has a factor of zero; its O is finite where the values are)
-#pragma unroll 2
+#pragma unroll (LEAN ? 1 : 2)
         for (int r0 = mw * RPW; r0 < rows; r0 += kFewMergers * RPW) {
           const int r = min(r0 + rr, ROWS - 1);   // (beyond the rows: read, not written)
           float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -403,7 +408,7 @@ __global__ void __launch_bounds__(few_threads(NR), 1)
     }
   } else {
     // ------------------------------------------------------------ consumers
-    set_registers<few_regs(NR), true>();
+    set_registers<few_regs(D, NR), true>();
     const int gi = lane >> 2, t = lane & 3;       // fragment row (or column), and place in it
     constexpr float LIFT = kRowsLiftF16;
     const int kpos = (gi >> 1) + 4 * (gi & 1);    // this lane's key of a half slice

@@ -12,9 +12,9 @@
 //                         then tables, reference counts and page bytes, spread
 //                         over all CTAs
 // Bound by the copied bytes where there are many (compacting, 482 MB read and written,
-// 82.6 us, 87 % of the copy rate; 192 samples of 12 prompts, 112 MB, 20.7 us, 81 %), else by the two
+// 82.6 us, 87 % of the copy rate; 192 samples of 12 prompts, 112 MB, 20.5 us, 82 %), else by the two
 // launches and some four loads that wait for one another in each (256 beams of 64
-// requests, 19 MB, 12.5 us; a pool of 230 slots 7.9).
+// requests, 19 MB, 12.1 us; a pool of 230 slots 7.5).
 // Which slots are taken depends on the counts alone, never on timing: reference
 // counts change by integer atomics, and every other word has one writer.  An
 // error found by the first kernel keeps the second from writing anything.

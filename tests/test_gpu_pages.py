@@ -76,6 +76,17 @@ def test_slots_over_several_chunks(slots):
     check_fork(p, list(range(n)), [1] * n)
 
 
+def test_slots_over_more_chunks_than_threads():
+    """300 chunks of slots, a third of them held by others."""
+    p = Pages(300 * 1024 + 5, 5, 1, 64, "fp4", 2, 2, seed=3)
+    for i in random.Random(3).sample(range(p.slots), p.slots // 3):
+        p.ref[i] = 1
+    for length in (130, 500, 1, 640):
+        p.add(length)
+    check_fork(p, [1, 1, 0, 3, 3, 3, 2, -1], [1, 128, 0, 0, 0, 0, 400, 513], in_place=True)
+    check_compact(p)
+
+
 def test_the_last_free_slot():
     p = Pages(12, 4, 1, 64, seed=1)
     p.add(300)

@@ -33,7 +33,7 @@
 // Measured, K/V bytes over time (head_dim 128, 4 KV heads): 64 requests of 1-8 k
 // positions, 8 rows a head 40.2 us (156 MB, 58 % of the copy rate: the pages arrive
 // at the full rate, start, split ends and join are 15 of the 40), 16 rows 50.4, 32
-// rows 78.7 (the matrix instructions alone 32, conversion 20, softmax 10); 256
+// rows 77.7 (the matrix instructions alone 32, conversion 20, softmax 10); 256
 // requests of 100-1500 49; one request over 60000 positions 21.4, over 8000 14.7.
 // One tile of rows_attn.cuh for each: 99, 97 and 98 us for 8, 16 and 32 rows.
 // Tried: K in tensor memory with tcgen05 and P V here (32 rows 109), all of it on
@@ -93,6 +93,49 @@ __device__ __forceinline__ void set_registers() {
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
+// Q tiles a0 .. a0 + AT - 1 (8 rows each) of an item: f16 in the fragments' order, and each row's scale; a whole warp.
+template <int D, int AT>
+__device__ __forceinline__ void few_q(const RowsAttnParams& p, int row0, int n, int h, int a0, uint4* frag, float* qscale, int lane) {
+  const RowsGeom& g = p.g;
+  const int gi = lane >> 2, t = lane & 3;
+  uint4 w[AT][D / 32];
+#pragma unroll
+  for (int a = 0; a < AT; ++a) {
+    const int r = 8 * (a0 + a) + gi, tk = r / g.group;
+    const uint4* src = reinterpret_cast<const uint4*>(
+        p.q + ((static_cast<int64_t>(row0) + tk) * g.num_q_heads + h * g.group + (r - tk * g.group)) * D + t * (D / 4));
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) w[a][i] = tk < n ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int a = 0; a < AT; ++a) {
+    // a power of two that brings the row's largest magnitude to [2^14, 2^15)
+    // (rows below 2^-40 are taken as 2^-40: the scale stays a normal number)
+    float amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      const uint32_t v[4] = {w[a][i].x, w[a][i].y, w[a][i].z, w[a][i].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        amax = max3(amax, fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xFFFF0000u)));
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -40);
+    const float mul = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
+    if (t == 0) qscale[8 * (a0 + a) + gi] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
+    // steps 2 i and 2 i + 1 of this lane's row: the products' B operand
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      uint32_t v[4] = {w[a][i].x, w[a][i].y, w[a][i].z, w[a][i].w};
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        v[x] = pack_f16(__uint_as_float(v[x] << 16) * mul, __uint_as_float(v[x] & 0xFFFF0000u) * mul);
+      frag[((a0 + a) * (D / 32) + i) * 32 + lane] = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+  }
+}
+
 template <int D, int NR>
 __global__ void __launch_bounds__(few_threads(NR), 1)
     rows_few_kernel(const __grid_constant__ CUtensorMap kv_map, const __grid_constant__ RowsAttnParams p) {
@@ -106,6 +149,9 @@ __global__ void __launch_bounds__(few_threads(NR), 1)
   constexpr int UPP = kPage / (16 * HT);       // of which a page has
   constexpr int SETS = CW / UPP;               // pages at a time
   constexpr bool QREG = few_q_regs(NR);
+  // 32 rows: a tile of the first piece's Q to a consumer each, which have nothing else to do yet (one request of 4 tokens
+  // over 900 positions 18.0 -> 16.5 us, 64 requests 78.6 -> 77.7; 16 rows, 64 requests: 50.4 -> 51.9)
+  constexpr bool FIRST = NR == 4;
   constexpr bool LEAN = few_other_regs(D, NR) < 56;   // few registers beside the consumers
   constexpr int QB = few_q_bytes(D, NR), QSCALE = NR * (D / 32) * 512;
   static_assert(CW % UPP == 0, "whole pages");
@@ -124,7 +170,8 @@ __global__ void __launch_bounds__(few_threads(NR), 1)
   uint64_t* qempty = qfull + 2;                                     // [2] and done with
   uint64_t* mfull = qempty + 2;                                     // every consumer's share of a piece is there
   uint64_t* mempty = mfull + 1;                                     // and joined
-  int* abortf = reinterpret_cast<int*>(mempty + 1);
+  uint64_t* qfirst = mempty + 1;                                    // the first piece's Q ready
+  int* abortf = reinterpret_cast<int*>(qfirst + 1);
   const Waits wt{g.err, abortf, p.wait_ns};
   int64_t* scan = reinterpret_cast<int64_t*>(smem + p.off_scan);
   RowsPiece* pieces = reinterpret_cast<RowsPiece*>(smem + p.off_pieces);
@@ -152,6 +199,7 @@ __global__ void __launch_bounds__(few_threads(NR), 1)
     }
     mbar_init(mfull, CW);
     mbar_init(mempty, kFewMergers);
+    mbar_init(qfirst, NR);
     *abortf = 0;
     fence_mbar_init();
   }
@@ -283,48 +331,12 @@ __global__ void __launch_bounds__(few_threads(NR), 1)
         const int sl = seq & 1;
         if (seq >= 2) ok = __all_sync(0xffffffffu, mbar_wait(&qempty[sl], static_cast<uint32_t>(seq / 2 - 1) & 1u, wt));
         if (!ok) break;
-        const int gi = lane >> 2, t = lane & 3;
-        uint4* frag = reinterpret_cast<uint4*>(qbuf + sl * QB);
-        float* qscale = reinterpret_cast<float*>(qbuf + sl * QB + QSCALE);
-        constexpr int AT = NR <= 2 ? NR : 2;   // tiles of rows at a time
-        uint4 w[AT][D / 32];
+        if (!FIRST || seq > 0) {
+          constexpr int AT = NR <= 2 ? NR : 2;   // tiles at a time
+          float* qscale = reinterpret_cast<float*>(qbuf + sl * QB + QSCALE);
 #pragma unroll 1
-        for (int a0 = 0; a0 < NR; a0 += AT) {
-#pragma unroll
-          for (int a = 0; a < AT; ++a) {
-            const int r = 8 * (a0 + a) + gi, tk = r / g.group;
-            const uint4* src = reinterpret_cast<const uint4*>(
-                p.q + ((static_cast<int64_t>(row0) + tk) * g.num_q_heads + h * g.group + (r - tk * g.group)) * D + t * (D / 4));
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) w[a][i] = tk < n ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-          }
-#pragma unroll
-          for (int a = 0; a < AT; ++a) {
-            // a power of two that brings the row's largest magnitude to [2^14, 2^15)
-            // (rows below 2^-40 are taken as 2^-40: the scale stays a normal number)
-            float amax = 0.f;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-              const uint32_t v[4] = {w[a][i].x, w[a][i].y, w[a][i].z, w[a][i].w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                amax = max3(amax, fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xFFFF0000u)));
-            }
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            const int e = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -40);
-            const float mul = __uint_as_float(static_cast<uint32_t>(127 + 14 - e) << 23);
-            if (t == 0) qscale[8 * (a0 + a) + gi] = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - 14 + e) << 23);
-            // steps 2 i and 2 i + 1 of this lane's row: the products' B operand
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-              uint32_t v[4] = {w[a][i].x, w[a][i].y, w[a][i].z, w[a][i].w};
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                v[x] = pack_f16(__uint_as_float(v[x] << 16) * mul, __uint_as_float(v[x] & 0xFFFF0000u) * mul);
-              frag[((a0 + a) * (D / 32) + i) * 32 + lane] = make_uint4(v[0], v[1], v[2], v[3]);
-            }
-          }
+          for (int a0 = 0; a0 < NR; a0 += AT)
+            few_q<D, AT>(p, row0, n, h, a0, reinterpret_cast<uint4*>(qbuf + sl * QB), qscale, lane);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&qfull[sl]);
@@ -421,13 +433,24 @@ __global__ void __launch_bounds__(few_threads(NR), 1)
       const int pk = seq % kRowsPieces;
       if (!__all_sync(0xffffffffu, mbar_wait(&ifull[pk], static_cast<uint32_t>(seq / kRowsPieces) & 1u, wt))) break;
       const int ctx = pieces[pk].ctx, n = pieces[pk].n, row0 = pieces[pk].row0, len = ctx + n, j0 = pieces[pk].j0, j1 = pieces[pk].j1;
+      [[maybe_unused]] const int h = pieces[pk].h;
       __syncwarp();
       if (lane == 0) mbar_arrive(&iempty[pk]);
       if (j1 == 0) break;
       const int qs = seq & 1;
+      if constexpr (FIRST) {
+        if (seq == 0) {
+          if (warp < NR) {
+            few_q<D, 1>(p, row0, n, h, warp, reinterpret_cast<uint4*>(qbuf), reinterpret_cast<float*>(qbuf + QSCALE), lane);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(qfirst);
+          }
+          if (!__all_sync(0xffffffffu, mbar_wait(qfirst, 0, wt))) break;
+        }
+      }
       const uint4* frag = reinterpret_cast<const uint4*>(qbuf + qs * QB) + lane;
       const float* qscale = reinterpret_cast<const float*>(qbuf + qs * QB + QSCALE);
-      if (!__all_sync(0xffffffffu, mbar_wait(&qfull[qs], static_cast<uint32_t>(seq / 2) & 1u, wt))) break;
+      if ((!FIRST || seq > 0) && !__all_sync(0xffffffffu, mbar_wait(&qfull[qs], static_cast<uint32_t>(seq / 2) & 1u, wt))) break;
       uint4 q[QREG ? NR : 1][QREG ? D / 32 : 1];
       if constexpr (QREG) {
 #pragma unroll
